@@ -17,7 +17,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libs3r.so")
 SOURCES = ["s3r_api.cu", "verify.cu", "verify_tc.cu", "draft.cu", "select.cu", "sampling.cu", "sched.cpp"]
-HEADERS = ["common.cuh", "attention.cuh", "kernels.h"]
+HEADERS = ["common.cuh", "attention.cuh", "draft_merge.cuh", "kernels.h", "tcgen05.cuh"]
 
 
 def nvcc_path() -> str:
