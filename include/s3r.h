@@ -215,6 +215,104 @@ S3R_API int s3r_sparse_draft_attn(const s3r_kv_cache* cache, const s3r_batch* ba
                           const int32_t* sel_count, void* out, float* lse, void* ws,
                           size_t ws_bytes, s3r_stream_t stream);
 
+/* ---------------------------------------------------------------- 8-bit cache ----------
+ * The same paged cache held in 8 bits: pools of e4m3 codes (1 sign, 4 exponent, 3 mantissa
+ * bits, largest value 448) in the layout of s3r_kv_cache, and one fp32 scale per (page, KV
+ * head) for K and for V: the value of a slot's element is code * scale. Half the bytes of the
+ * bf16 cache, so the verify and the draft read half as much. Selection, sampling and commit
+ * are those of the bf16 cache (s3r_select_kv and its relatives take &cache->pools; of the
+ * pools they read nothing).
+ *
+ * Rows enter by s3r_kv8_append; attention reads the cache alone, so a step's own rows are
+ * appended before its attention call (draft step i: one row at L+i; verify: the k+1 rows at
+ * L..L+k, which replaces the drafts' rows). Two requests that share a page may both read it;
+ * a page that receives rows belongs to one request.
+ *
+ * Scales are >= 0 and finite; any other scale read is taken as 0 and sets S3R_ERR_NONFINITE.
+ * s3r_kv8_append writes powers of two, the attention calls take any. */
+typedef struct {
+  s3r_kv_cache pools;        /* k_pool, v_pool: e4m3 [num_pages][num_kv_heads][16][head_dim], 16-byte aligned */
+  float* k_scale;            /* [num_pages][num_kv_heads] */
+  float* v_scale;
+} s3r_kv8_cache;
+
+/* Bytes of workspace for every call of a round over an 8-bit cache (append, draft, verify,
+ * selection, sampling; page calls too), arguments as s3r_workspace_size. Host function; the
+ * size depends on the current device's SM count. */
+S3R_API size_t s3r_kv8_workspace_size(const s3r_kv8_cache* cache, int32_t num_requests,
+                              int32_t max_pages_per_req, int32_t max_k, int32_t vocab,
+                              int32_t sel_stride);
+
+/* Write rows into the cache. Request r's rows t < n_new[r] go to positions
+ * L + first[r] + t (L = seq_lens[r]; first == NULL: 0; n_new == NULL: T rows each).
+ *   k_new, v_new  bf16: request r's rows [T][H_kv][d] start at k_new + r * kv_stride
+ *                 (elements, a multiple of 8; 0 means T * H_kv * d); rows t >= n_new[r] are
+ *                 not read. 16-byte aligned.
+ * For every page that receives a row, KV head, and K and V apart: the live rows are the
+ * page's positions below L + first[r] (kept, at their old scale) and the new ones; the scale
+ * becomes 2^e, e the least integer >= -126 with max |x| <= 448 * 2^e over them (1 if all are
+ * zero), and the live rows' codes e4m3(x / 2^e), round to nearest even. Slots behind the last
+ * new row keep their codes. NaN and infinite elements, of kept rows too, are stored as 0 and
+ * set S3R_ERR_NONFINITE. Rows past the page table's capacity, n_new outside [0, T] or first < 0
+ * skip the request, a page id outside the pool skips the page (S3R_ERR_DEVICE_BOUNDS). */
+S3R_API int s3r_kv8_append(const s3r_kv8_cache* cache, const s3r_batch* batch, const int32_t* first,
+                   int32_t T, const int32_t* n_new, const void* k_new, const void* v_new,
+                   int64_t kv_stride, void* ws, size_t ws_bytes, s3r_stream_t stream);
+
+/* Dense verify attention over an 8-bit cache: rows t = 0..k of request r at positions L+t,
+ * row t of each query head attending positions 0..L+t of the cache (k = 0: one decode row).
+ * q, out, lse, score_logits as for s3r_verify_attn; sums, maxima and logits in fp32. */
+S3R_API int s3r_verify_attn_kv8(const s3r_kv8_cache* cache, const s3r_batch* batch, int32_t k,
+                        const void* q, void* out, float* lse, float* score_logits, void* ws,
+                        size_t ws_bytes, s3r_stream_t stream);
+
+/* Sparse self-draft attention over an 8-bit cache: step i = draft_step[r]'s query rows attend
+ * the selected positions and L..L+i. Arguments as s3r_sparse_draft_attn (the step's row is in
+ * the cache already). */
+S3R_API int s3r_sparse_draft_attn_kv8(const s3r_kv8_cache* cache, const s3r_batch* batch,
+                              const int32_t* draft_step, const void* q, int64_t q_stride,
+                              const int32_t* sel_idx, int32_t sel_stride,
+                              const int32_t* sel_count, void* out, float* lse, void* ws,
+                              size_t ws_bytes, s3r_stream_t stream);
+
+/* ------------------------------------------------------ page tables on the GPU ----------
+ * The pages of a pool that no request holds are a stack: free_pages[0 .. free_count - 1]
+ * (free_pages int32 [free_capacity], free_count int32 [1]). held[r] (int32 [num_requests])
+ * is how many leading entries of request r's page-table row are its pages. Both calls work
+ * for a bf16 and an 8-bit cache, take the requests in batch order, give results that depend
+ * on the inputs alone, and write the new counts to held_out / free_count_out, which may be
+ * held / free_count themselves (otherwise entries of requests outside the batch are not
+ * written). batch->page_table is not used; batch->max_pages_per_req is. */
+S3R_API size_t s3r_pages_workspace_size(int32_t num_requests);
+
+/* Room for the next tokens: request r at committed length L gets what it lacks of
+ * ceil((L + n_new[r]) / 16) pages (n_new == NULL: T tokens each; 0 <= n_new[r] <= T). The i-th
+ * new page of a request, after the `before` pages its predecessors in the batch asked for, is
+ * free_pages[free_count - 1 - before - i], entered at page_table[r][held[r] + i]. A request
+ * whose pages would go past the stack's last one gets none, nor do later ones that need any:
+ * granted[r] = 0, no error (1 for every request that has its pages).
+ *   slot_map  int64 [num_requests][T] or NULL: page * 16 + slot of position L + t for
+ *             t < n_new[r], -1 for the other t and for requests not served.
+ * seq_lens, n_new or held out of range, or more pages than max_pages_per_req, leave the
+ * request as it is with granted[r] = 0; these and a free_count outside [0, free_capacity]
+ * set S3R_ERR_DEVICE_BOUNDS. */
+S3R_API int s3r_alloc_pages(const s3r_batch* batch, int32_t* page_table, int32_t T,
+                    const int32_t* n_new, const int32_t* held, const int32_t* free_pages,
+                    const int32_t* free_count, int32_t free_capacity, int32_t* held_out,
+                    int32_t* free_count_out, int32_t* granted, int64_t* slot_map, void* ws,
+                    size_t ws_bytes, s3r_stream_t stream);
+
+/* Pages back to the stack: request r keeps min(held[r], ceil(keep_len[r] / 16)) pages
+ * (keep_len == NULL: none) and the others, in table order, go to free_pages[free_count +
+ * before + i]. The table's entries stay as they are (those at held_out[r] and after mean
+ * nothing). A request whose pages do not fit below free_capacity keeps them, as do later ones
+ * that have any to give (S3R_ERR_DEVICE_BOUNDS); held or keep_len out of range likewise.
+ * batch->seq_lens is not read. */
+S3R_API int s3r_release_pages(const s3r_batch* batch, const int32_t* page_table,
+                      const int32_t* keep_len, const int32_t* held, int32_t* free_pages,
+                      const int32_t* free_count, int32_t free_capacity, int32_t* held_out,
+                      int32_t* free_count_out, void* ws, size_t ws_bytes, s3r_stream_t stream);
+
 /* Normaliser of one row of logits x: max = max_v x_v and sum = sum_v exp(x_v - max), so that
  * softmax(x)_v = exp(x_v - max) / sum (non-finite entries count as -inf). 16 bytes. */
 typedef struct s3r_row_norm {

@@ -45,6 +45,10 @@ class BatchDesc(ctypes.Structure):
                 ("page_table", ctypes.c_void_p), ("max_pages_per_req", ctypes.c_int32)]
 
 
+class KV8CacheDesc(ctypes.Structure):
+    _fields_ = [("pools", KVCacheDesc), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
 class SchedConfig(ctypes.Structure):
     _fields_ = [("capacity", ctypes.c_int32), ("policy", ctypes.c_int32), ("evict", ctypes.c_int32),
                 ("cap0", ctypes.c_int32), ("cap_min", ctypes.c_int32), ("cap_max", ctypes.c_int32),
@@ -68,7 +72,15 @@ def _load():
     lib = ctypes.CDLL(LIB_PATH)
     P, I32, I64, U64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_size_t
     C, B = ctypes.POINTER(KVCacheDesc), ctypes.POINTER(BatchDesc)
+    C8 = ctypes.POINTER(KV8CacheDesc)
     sig = {
+        "s3r_kv8_workspace_size": (SZ, [C8, I32, I32, I32, I32, I32]),
+        "s3r_kv8_append": (ctypes.c_int, [C8, B, P, I32, P, P, P, I64, P, SZ, P]),
+        "s3r_verify_attn_kv8": (ctypes.c_int, [C8, B, I32, P, P, P, P, P, SZ, P]),
+        "s3r_sparse_draft_attn_kv8": (ctypes.c_int, [C8, B, P, P, I64, P, I32, P, P, P, P, SZ, P]),
+        "s3r_pages_workspace_size": (SZ, [I32]),
+        "s3r_alloc_pages": (ctypes.c_int, [B, P, I32, P, P, P, P, I32, P, P, P, P, P, SZ, P]),
+        "s3r_release_pages": (ctypes.c_int, [B, P, P, P, P, P, I32, P, P, P, SZ, P]),
         "s3r_workspace_size": (SZ, [C, I32, I32, I32, I32, I32]),
         "s3r_workspace_init": (ctypes.c_int, [P, SZ, P]),
         "s3r_verify_attn": (ctypes.c_int, [C, B, I32, P, P, P, P, P, P, P, SZ, P]),
@@ -166,6 +178,7 @@ def make_batch(seq_lens: torch.Tensor, page_table: torch.Tensor | None = None,
                      _ptr(seq_lens, torch.int32, "seq_lens").value,
                      pt.value if pt is not None else None, mp)
     desc._refs = (seq_lens, page_table, req_ids)
+    desc._device = seq_lens.device
     return desc
 
 
@@ -279,6 +292,196 @@ def s3r_sparse_draft_attn(cache, batch, draft_step, q, k_new, v_new, sel_idx, se
         _ptr(sel_idx, i32, "sel_idx"), sel_idx.shape[-1], _ptr(sel_count, i32, "sel_count"),
         _ptr(out, bf, "out"), _ptr(lse, torch.float32, "lse", allow_none=True),
         _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)), "s3r_sparse_draft_attn")
+
+# ------------------------------------------------------------- 8-bit cache, page tables ----
+def _arg(t, dtype, shape, what, device, allow_none=False):
+    """Address of a contiguous CUDA tensor of this dtype, shape and device. `dtype` may be a
+    tuple of accepted dtypes."""
+    if t is None:
+        if allow_none:
+            return None
+        raise ValueError(f"{what} is required")
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what} must be a torch.Tensor")
+    if t.dtype != dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    if t.device != device:
+        raise ValueError(f"{what} must be on {device}, is on {t.device}")
+    return t.data_ptr()
+
+
+def _call_device(*descs):
+    """The device of the descriptors' tensors, which must be the current one (the stream and the
+    launch are the current device's)."""
+    device = descs[0]._device
+    if any(d._device != device for d in descs):
+        raise ValueError("cache and batch are on different devices")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+    return device
+
+
+def _ws_arg(ws, device):
+    if not isinstance(ws, torch.Tensor) or ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != device:
+        raise TypeError(f"ws must be a contiguous uint8 tensor on {device}")
+    return ws.data_ptr(), ws.numel()
+
+
+def _batch_table(batch):
+    """(num_requests, page table) of a batch made with a page table."""
+    seq_lens, pt, req_ids = batch._refs
+    if pt is None:
+        raise ValueError("the batch needs a page table")
+    if pt.shape[0] != batch.num_requests:
+        raise ValueError(f"the page table has {pt.shape[0]} rows for {batch.num_requests} requests")
+    if pt.device != seq_lens.device or (req_ids is not None and req_ids.device != seq_lens.device):
+        raise ValueError("the batch's tensors are on different devices")
+    return batch.num_requests, pt
+
+
+def _stream_ptr(stream):
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def make_kv8_cache(k_pool: torch.Tensor, v_pool: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                   num_q_heads: int) -> KV8CacheDesc:
+    """Descriptor of an 8-bit cache: pools [num_pages][num_kv_heads][16][head_dim] of
+    torch.float8_e4m3fn (or uint8 codes), scales fp32 [num_pages][num_kv_heads]."""
+    f8 = (torch.float8_e4m3fn, torch.uint8)
+    if not isinstance(k_pool, torch.Tensor) or k_pool.dim() != 4 or k_pool.shape[2] != PAGE_SIZE:
+        raise ValueError("pools must be [num_pages][num_kv_heads][16][head_dim] and equal")
+    if k_pool.device.type != "cuda":
+        raise ValueError("k_pool must be a CUDA tensor")
+    P, H, S, D = k_pool.shape
+    dev = k_pool.device
+    kp, vp = _arg(k_pool, f8, k_pool.shape, "k_pool", dev), _arg(v_pool, f8, k_pool.shape, "v_pool", dev)
+    ks, vs = (_arg(t, torch.float32, (P, H), n, dev) for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")))
+    desc = KV8CacheDesc(KVCacheDesc(num_q_heads, H, D, S, P, kp, vp), ks, vs)
+    desc._refs = (k_pool, v_pool, k_scale, v_scale)
+    desc._device = dev
+    return desc
+
+
+def s3r_kv8_workspace_size(cache: KV8CacheDesc, num_requests: int, max_pages_per_req: int, max_k: int,
+                           vocab: int, sel_stride: int) -> int:
+    n = _lib.s3r_kv8_workspace_size(ctypes.byref(cache), num_requests, max_pages_per_req, max_k, vocab, sel_stride)
+    if n == 0:
+        raise S3RError(1, "s3r_kv8_workspace_size")
+    return int(n)
+
+
+def s3r_kv8_append(cache, batch, k_new, v_new, ws, *, first=None, n_new=None, stream=None):
+    """k_new, v_new: bf16 [NR][T][H_kv][d], each request's rows contiguous (a view such as
+    block[:, i:i+1] of a longer block will do); first, n_new: int32 [NR] or None."""
+    dev = _call_device(cache, batch)
+    nr, _ = _batch_table(batch)
+    c = cache.pools
+    if not isinstance(k_new, torch.Tensor) or k_new.dim() != 4:
+        raise ValueError("k_new must be [num_requests][T][num_kv_heads][head_dim]")
+    T, inner = k_new.shape[1], (c.num_kv_heads * c.head_dim, c.head_dim, 1)
+    stride = None
+    for t, what in ((k_new, "k_new"), (v_new, "v_new")):
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.device != dev:
+            raise TypeError(f"{what} must be a bf16 tensor on {dev}")
+        if t.shape != (nr, T, c.num_kv_heads, c.head_dim):
+            raise ValueError(f"{what} must be [{nr}][{T}][{c.num_kv_heads}][{c.head_dim}], got {tuple(t.shape)}")
+        if t.numel() and any(n > 1 and s != w for n, s, w in zip(t.shape[1:], t.stride()[1:], inner)):
+            raise ValueError(f"{what}: each request's rows must be contiguous")
+        own = t.stride(0) if nr > 1 else T * inner[0]
+        if stride is not None and own != stride:
+            raise ValueError("k_new and v_new must share a request stride")
+        stride = own
+    i32 = torch.int32
+    wp, wn = _ws_arg(ws, dev)
+    _check(_lib.s3r_kv8_append(
+        ctypes.byref(cache), ctypes.byref(batch), _arg(first, i32, (nr,), "first", dev, True), T,
+        _arg(n_new, i32, (nr,), "n_new", dev, True), k_new.data_ptr(), v_new.data_ptr(), stride, wp, wn,
+        _stream_ptr(stream)), "s3r_kv8_append")
+
+
+def s3r_verify_attn_kv8(cache, batch, k, q, out, lse, score_logits, ws, stream=None):
+    """q, out bf16 [NR][k+1][H_q][d], lse fp32 [NR][k+1][H_q], score_logits fp32
+    [NR][H_kv][G*(k+1)][capacity] or None."""
+    dev = _call_device(cache, batch)
+    nr, pt = _batch_table(batch)
+    c = cache.pools
+    bf, f32 = torch.bfloat16, torch.float32
+    T, G = k + 1, c.num_q_heads // max(1, c.num_kv_heads)
+    rows = (nr, T, c.num_q_heads, c.head_dim)
+    wp, wn = _ws_arg(ws, dev)
+    _check(_lib.s3r_verify_attn_kv8(
+        ctypes.byref(cache), ctypes.byref(batch), k, _arg(q, bf, rows, "q", dev), _arg(out, bf, rows, "out", dev),
+        _arg(lse, f32, rows[:3], "lse", dev),
+        _arg(score_logits, f32, (nr, c.num_kv_heads, G * T, pt.shape[1] * PAGE_SIZE), "score_logits", dev, True),
+        wp, wn, _stream_ptr(stream)), "s3r_verify_attn_kv8")
+
+
+def s3r_sparse_draft_attn_kv8(cache, batch, draft_step, q, sel_idx, sel_count, out, lse, ws, stream=None):
+    """q bf16 [NR][H_q][d], possibly a view with strided requests (q_block[:, i]); sel_idx int32
+    [NR][H_kv][stride], sel_count int32 [NR][H_kv]; out bf16 [NR][H_q][d]; lse fp32 [NR][H_q] or None."""
+    dev = _call_device(cache, batch)
+    nr, _ = _batch_table(batch)
+    c = cache.pools
+    i32, rows = torch.int32, (nr, c.num_q_heads, c.head_dim)
+    if not isinstance(q, torch.Tensor) or q.dtype != torch.bfloat16 or q.device != dev:
+        raise TypeError(f"q must be a bf16 tensor on {dev}")
+    if q.shape != rows or any(n > 1 and s != w for n, s, w in zip(rows[1:], q.stride()[1:], (c.head_dim, 1))):
+        raise ValueError(f"q must be {list(rows)} with contiguous rows, got {tuple(q.shape)}")
+    if not isinstance(sel_idx, torch.Tensor) or sel_idx.dim() != 3:
+        raise ValueError("sel_idx must be [num_requests][num_kv_heads][stride]")
+    wp, wn = _ws_arg(ws, dev)
+    _check(_lib.s3r_sparse_draft_attn_kv8(
+        ctypes.byref(cache), ctypes.byref(batch), _arg(draft_step, i32, (nr,), "draft_step", dev), q.data_ptr(),
+        q.stride(0) if nr > 1 else rows[1] * rows[2],
+        _arg(sel_idx, i32, (nr, c.num_kv_heads, sel_idx.shape[2]), "sel_idx", dev), sel_idx.shape[2],
+        _arg(sel_count, i32, (nr, c.num_kv_heads), "sel_count", dev),
+        _arg(out, torch.bfloat16, rows, "out", dev), _arg(lse, torch.float32, rows[:2], "lse", dev, True),
+        wp, wn, _stream_ptr(stream)), "s3r_sparse_draft_attn_kv8")
+
+
+def s3r_pages_workspace_size(num_requests: int) -> int:
+    n = _lib.s3r_pages_workspace_size(num_requests)
+    if n == 0:
+        raise S3RError(1, "s3r_pages_workspace_size")
+    return int(n)
+
+
+def _pages_args(batch, held, free_pages, free_count, held_out, free_count_out):
+    dev = _call_device(batch)
+    nr, pt = _batch_table(batch)
+    i32 = torch.int32
+    if not isinstance(free_pages, torch.Tensor) or free_pages.dim() != 1:
+        raise ValueError("free_pages must be one-dimensional")
+    return (dev, nr, pt.data_ptr(), _arg(held, i32, (nr,), "held", dev),
+            _arg(free_pages, i32, free_pages.shape, "free_pages", dev),
+            _arg(free_count, i32, (1,), "free_count", dev), free_pages.shape[0],
+            _arg(held_out, i32, (nr,), "held_out", dev), _arg(free_count_out, i32, (1,), "free_count_out", dev))
+
+
+def s3r_alloc_pages(batch, T, held, free_pages, free_count, held_out, free_count_out, granted, ws, *, n_new=None,
+                    slot_map=None, stream=None):
+    """Pages for T (or n_new[r] <= T) more tokens of each request, entered into the batch's page
+    table; slot_map int64 [NR][T] or None. held_out / free_count_out may be held / free_count."""
+    dev, nr, pt, hp, fp, fc, cap, ho, fo = _pages_args(batch, held, free_pages, free_count, held_out, free_count_out)
+    wp, wn = _ws_arg(ws, dev)
+    _check(_lib.s3r_alloc_pages(
+        ctypes.byref(batch), pt, T, _arg(n_new, torch.int32, (nr,), "n_new", dev, True), hp, fp, fc, cap, ho, fo,
+        _arg(granted, torch.int32, (nr,), "granted", dev),
+        _arg(slot_map, torch.int64, (nr, T), "slot_map", dev, True), wp, wn, _stream_ptr(stream)), "s3r_alloc_pages")
+
+
+def s3r_release_pages(batch, held, free_pages, free_count, held_out, free_count_out, ws, *, keep_len=None,
+                      stream=None):
+    """Pages beyond ceil(keep_len[r] / 16) (None: all) of each request back to the stack."""
+    dev, nr, pt, hp, fp, fc, cap, ho, fo = _pages_args(batch, held, free_pages, free_count, held_out, free_count_out)
+    wp, wn = _ws_arg(ws, dev)
+    _check(_lib.s3r_release_pages(
+        ctypes.byref(batch), pt, _arg(keep_len, torch.int32, (nr,), "keep_len", dev, True), hp, fp, fc, cap, ho, fo,
+        wp, wn, _stream_ptr(stream)), "s3r_release_pages")
 
 
 def _norms(t, what):

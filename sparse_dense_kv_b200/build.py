@@ -16,8 +16,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libs3r.so")
-SOURCES = ["s3r_api.cu", "verify.cu", "verify_tc.cu", "draft.cu", "select.cu", "sampling.cu", "sched.cpp"]
-HEADERS = ["common.cuh", "attention.cuh", "draft_merge.cuh", "kernels.h", "tcgen05.cuh"]
+SOURCES = ["s3r_api.cu", "verify.cu", "verify_tc.cu", "draft.cu", "select.cu", "sampling.cu", "verify_kv8.cu",
+           "draft_kv8.cu", "append_kv8.cu", "pages.cu", "sched.cpp"]
+HEADERS = ["common.cuh", "attention.cuh", "draft_merge.cuh", "kernels.h", "kv8.cuh", "tcgen05.cuh"]
 
 
 def nvcc_path() -> str:

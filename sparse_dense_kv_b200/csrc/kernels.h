@@ -115,6 +115,103 @@ struct SampleParams {
   s3r_row_norm* q_norm;        // optional: draft rows' normalisers [NR][k] (draft: out, spec: in)
 };
 
+// 8-bit cache: e4m3 pools of the same layout, fp32 scales [num_pages][Hkv] for K and for V.
+struct VerifyKv8Params {
+  const int32_t* req_ids;
+  const int32_t* seq_lens;
+  const int32_t* page_table;
+  int max_pages;
+  int cap;                 // 16 * max_pages
+  int Hq, Hkv, G, T, R, Rp;
+  int64_t num_pages;
+  const float* k_scale;
+  const float* v_scale;
+  const __nv_bfloat16* q;
+  __nv_bfloat16* out;
+  float* lse;
+  float* scores;
+  float scale;
+  int* err;
+  int* sched;              // [2] span counter, exited CTAs (zero between launches)
+  int* plan;               // span length, span prefix (written by the attention kernel for the merge)
+  float* part;             // span records [span][m: Rp][l: Rp][O: Rp][D]
+  int req_off;
+  int wait_limit;
+  int num_requests;
+};
+
+struct DraftKv8Params {
+  const int32_t* req_ids;
+  const int32_t* seq_lens;
+  const int32_t* page_table;
+  int max_pages;
+  int cap;
+  int Hq, Hkv, G;
+  int64_t num_pages;
+  const uint8_t* k_pool;
+  const uint8_t* v_pool;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* draft_step;
+  const __nv_bfloat16* q;
+  int64_t q_stride;        // elements between consecutive requests
+  const int32_t* sel_idx;
+  int sel_stride;
+  const int32_t* sel_count;
+  __nv_bfloat16* out;
+  float* lse;
+  float scale;
+  int* err;
+  int* tickets;
+  float* part;             // chunk records [launch-local request][Hkv][nchunk_max]
+  int chunk, nchunk_max;
+  int num_requests;
+};
+
+struct AppendKv8Params {
+  const int32_t* req_ids;
+  const int32_t* seq_lens;
+  const int32_t* page_table;
+  int max_pages;
+  int cap;
+  int Hkv;
+  int64_t num_pages;
+  uint8_t* k_pool;
+  uint8_t* v_pool;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* first;    // offset of row 0 from the committed length, or NULL (0)
+  const int32_t* n_new;    // rows per request, or NULL (T)
+  int T;
+  const __nv_bfloat16* k_new;
+  const __nv_bfloat16* v_new;
+  int64_t kv_stride;       // elements between consecutive requests
+  int* err;
+  int num_requests;
+};
+
+struct PagesParams {
+  const int32_t* req_ids;
+  const int32_t* seq_lens;
+  int32_t* page_table;
+  int max_pages;
+  int batch, num_requests;
+  const int32_t* n_new;    // alloc: tokens per request, or NULL (T)
+  const int32_t* keep_len; // release: positions kept, or NULL (0)
+  int T;
+  const int32_t* held;
+  int32_t* free_pages;
+  const int32_t* free_count;
+  int free_capacity;       // release: entries of free_pages
+  int32_t* held_out;
+  int32_t* free_count_out;
+  int32_t* granted;
+  int64_t* slot_map;       // or NULL
+  int* err;
+  int* ticket;
+  int rp;                  // requests per CTA
+};
+
 // Record the CUDA error behind an S3R_ERR_CUDA status (readable by s3r_last_error_message)
 // and return S3R_ERR_CUDA; returns S3R_OK for cudaSuccess.
 int cuda_status(cudaError_t e, const char* where);
@@ -154,6 +251,22 @@ size_t sample_partial_bytes(int num_requests, int k, int vocab);
 void spec_offsets(int num_requests, int k, int vocab, size_t* plan_off, size_t* draw_off, size_t* sub_off);
 // Byte offset of draft sampling's sub-block sums in its partials area.
 size_t draft_sub_offset(int num_requests, int vocab);
+
+int launch_verify_kv8(const CUtensorMap& k1, const CUtensorMap& v1, const CUtensorMap& k8,
+                      const CUtensorMap& v8, const VerifyKv8Params& p, int D, int batch, int num_sms,
+                      cudaStream_t stream, int* launches);
+size_t verify_kv8_bytes(int num_requests, int Hkv, int R, int D, int num_sms);
+int verify_kv8_rec_rows(int R);
+int verify_kv8_plan_bytes();
+
+int launch_draft_kv8(const DraftKv8Params& p, int D, int batch, cudaStream_t stream);
+int draft_kv8_chunk(int pairs, int sel_stride, int num_sms);   // positions per CTA
+size_t draft_kv8_bytes(int num_requests, int Hkv, int sel_stride, int D, int num_sms);
+
+int launch_append_kv8(const AppendKv8Params& p, int D, int batch, cudaStream_t stream);
+
+int launch_alloc_pages(const PagesParams& p, cudaStream_t stream);
+int launch_release_pages(const PagesParams& p, cudaStream_t stream);
 
 int launch_commit(const int32_t* req_ids, int batch, int num_requests, int k, const int32_t* n_out,
                   int32_t* seq_lens, int64_t* stats, cudaStream_t stream);

@@ -169,6 +169,38 @@ int make_paged_map(CUtensorMap* map, void* pool, const s3r_kv_cache* c, int page
   return S3R_OK;
 }
 
+// 4-D view of an e4m3 pool (d, slot, kv head, page) with boxes of 128 bytes x 16 slots x 1 head x
+// `pages` pages (128-byte swizzle): a tile row is 128 bytes whatever head_dim is; at 64 the
+// second half of the box lies outside the pool's innermost extent and reads as zeros.
+int make_kv8_map(CUtensorMap* map, void* pool, const s3r_kv_cache* c, int pages) {
+  auto fn = encode_fn();
+  if (!fn) {
+    std::snprintf(g_last_error, sizeof(g_last_error), "cuTensorMapEncodeTiled unavailable");
+    return S3R_ERR_CUDA;
+  }
+  const cuuint64_t row = (cuuint64_t)c->head_dim;
+  cuuint64_t dims[4] = {row, (cuuint64_t)S3R_PAGE_SIZE, (cuuint64_t)c->num_kv_heads, (cuuint64_t)c->num_pages};
+  cuuint64_t strides[3] = {row, row * S3R_PAGE_SIZE, row * S3R_PAGE_SIZE * c->num_kv_heads};
+  cuuint32_t box[4] = {128, (cuuint32_t)S3R_PAGE_SIZE, 1, (cuuint32_t)pages};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, pool, dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    std::snprintf(g_last_error, sizeof(g_last_error), "cuTensorMapEncodeTiled (e4m3 pool): error %d", (int)r);
+    return S3R_ERR_CUDA;
+  }
+  return S3R_OK;
+}
+
+int check_kv8_cache(const s3r_kv8_cache* c) {
+  if (!c) return S3R_ERR_INVALID_ARG;
+  const int st = check_cache(&c->pools);
+  if (st != S3R_OK) return st;
+  if (!c->k_scale || !c->v_scale || !aligned4(c->k_scale) || !aligned4(c->v_scale)) return S3R_ERR_INVALID_ARG;
+  return S3R_OK;
+}
+
 // 3-D view of the query rows q [num_requests][T][H_q][d] as (d, q head, request * T + t)
 // with boxes of 64 columns x G heads x T rows: the G*T rows of one (request, KV head) land
 // as one [T*G][128 B] block (row t*G + g, 128-byte swizzle) per 64-column half.
@@ -570,6 +602,242 @@ int s3r_sparse_draft_attn(const s3r_kv_cache* cache, const s3r_batch* batch,
   const int st = launch_draft(p, cache->head_dim, batch->batch, sm_count(), (cudaStream_t)stream, &nl);
   g_launches.fetch_add((uint64_t)nl, std::memory_order_relaxed);
   return st;
+}
+
+size_t s3r_kv8_workspace_size(const s3r_kv8_cache* cache, int32_t num_requests, int32_t max_pages_per_req,
+                              int32_t max_k, int32_t vocab, int32_t sel_stride) {
+  if (check_kv8_cache(cache) != S3R_OK || num_requests < 0 || max_pages_per_req <= 0 || max_k < 0 ||
+      max_k > S3R_MAX_K || vocab < 0 || sel_stride < 0 ||
+      (int64_t)max_pages_per_req * S3R_PAGE_SIZE >= ((int64_t)1 << 30))
+    return 0;
+  const s3r_kv_cache* c = &cache->pools;
+  const int cap = max_pages_per_req * S3R_PAGE_SIZE, sms = sm_count();
+  const int G = c->num_q_heads / c->num_kv_heads;
+  const int rows = G * (max_k + 1) < S3R_MAX_ROWS ? G * (max_k + 1) : S3R_MAX_ROWS;
+  size_t part = verify_kv8_bytes(num_requests, c->num_kv_heads, rows, c->head_dim, sms);
+  const size_t b = draft_kv8_bytes(num_requests, c->num_kv_heads, sel_stride, c->head_dim, sms);
+  const size_t d = select_sigma_bytes(num_requests, c->num_kv_heads, cap);
+  const size_t e = sample_partial_bytes(num_requests, max_k, vocab > 0 ? vocab : 1);
+  if (b > part) part = b;
+  if (d > part) part = d;
+  if (e > part) part = e;
+  return head_bytes(num_requests) + part;
+}
+
+int s3r_kv8_append(const s3r_kv8_cache* cache, const s3r_batch* batch, const int32_t* first, int32_t T,
+                   const int32_t* n_new, const void* k_new, const void* v_new, int64_t kv_stride, void* ws,
+                   size_t ws_bytes, s3r_stream_t stream) {
+  S3R_TRY(check_kv8_cache(cache));
+  S3R_TRY(check_batch(batch, true));
+  if (T < 0) return S3R_ERR_INVALID_ARG;
+  if (!k_new || !v_new || !aligned16(k_new) || !aligned16(v_new) || (first && !aligned4(first)) ||
+      (n_new && !aligned4(n_new)))
+    return S3R_ERR_INVALID_ARG;
+  const s3r_kv_cache* c = &cache->pools;
+  const int64_t least = (int64_t)T * c->num_kv_heads * c->head_dim;
+  if (kv_stride == 0) kv_stride = least;
+  if (kv_stride < least || (kv_stride % 8)) return S3R_ERR_INVALID_ARG;
+  if (batch->batch == 0 || T == 0) return S3R_OK;
+  S3R_TRY(check_ws(ws, ws_bytes, head_bytes(batch->num_requests)));
+  const Carve w = carve(ws, batch->num_requests);
+  AppendKv8Params p;
+  std::memset(&p, 0, sizeof(p));
+  p.req_ids = batch->req_ids;
+  p.seq_lens = batch->seq_lens;
+  p.page_table = batch->page_table;
+  p.max_pages = batch->max_pages_per_req;
+  p.cap = batch->max_pages_per_req * S3R_PAGE_SIZE;
+  p.Hkv = c->num_kv_heads;
+  p.num_pages = c->num_pages;
+  p.k_pool = static_cast<uint8_t*>(c->k_pool);
+  p.v_pool = static_cast<uint8_t*>(c->v_pool);
+  p.k_scale = cache->k_scale;
+  p.v_scale = cache->v_scale;
+  p.first = first;
+  p.n_new = n_new;
+  p.T = T;
+  p.k_new = static_cast<const __nv_bfloat16*>(k_new);
+  p.v_new = static_cast<const __nv_bfloat16*>(v_new);
+  p.kv_stride = kv_stride;
+  p.err = w.err;
+  p.num_requests = batch->num_requests;
+  return finish(launch_append_kv8(p, c->head_dim, batch->batch, (cudaStream_t)stream), 1);
+}
+
+int s3r_verify_attn_kv8(const s3r_kv8_cache* cache, const s3r_batch* batch, int32_t k, const void* q,
+                        void* out, float* lse, float* score_logits, void* ws, size_t ws_bytes,
+                        s3r_stream_t stream) {
+  S3R_TRY(check_kv8_cache(cache));
+  S3R_TRY(check_batch(batch, true));
+  const s3r_kv_cache* c = &cache->pools;
+  if (k < 0 || k > S3R_MAX_K) return S3R_ERR_UNSUPPORTED;
+  const int G = c->num_q_heads / c->num_kv_heads, R = G * (k + 1);
+  if (R > S3R_MAX_ROWS) return S3R_ERR_UNSUPPORTED;
+  if (!q || !out || !lse || !aligned16(q) || !aligned16(out) || !aligned4(lse) ||
+      (score_logits && !aligned16(score_logits)))
+    return S3R_ERR_INVALID_ARG;
+  if (batch->batch == 0) return S3R_OK;
+  const int sms = sm_count();
+  S3R_TRY(check_ws(ws, ws_bytes, head_bytes(batch->num_requests) +
+                                     verify_kv8_bytes(batch->num_requests, c->num_kv_heads, R, c->head_dim, sms)));
+  CUtensorMap k1, v1, k8, v8;
+  S3R_TRY(make_kv8_map(&k1, c->k_pool, c, 1));
+  S3R_TRY(make_kv8_map(&v1, c->v_pool, c, 1));
+  S3R_TRY(make_kv8_map(&k8, c->k_pool, c, 8));
+  S3R_TRY(make_kv8_map(&v8, c->v_pool, c, 8));
+  const Carve w = carve(ws, batch->num_requests);
+  VerifyKv8Params p;
+  std::memset(&p, 0, sizeof(p));
+  p.req_ids = batch->req_ids;
+  p.seq_lens = batch->seq_lens;
+  p.page_table = batch->page_table;
+  p.max_pages = batch->max_pages_per_req;
+  p.cap = batch->max_pages_per_req * S3R_PAGE_SIZE;
+  p.Hq = c->num_q_heads;
+  p.Hkv = c->num_kv_heads;
+  p.G = G;
+  p.T = k + 1;
+  p.R = R;
+  p.Rp = verify_kv8_rec_rows(R);
+  p.num_pages = c->num_pages;
+  p.k_scale = cache->k_scale;
+  p.v_scale = cache->v_scale;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.scores = score_logits;
+  p.scale = 1.0f / sqrtf((float)c->head_dim);
+  p.err = w.err;
+  p.sched = w.sched;
+  p.plan = reinterpret_cast<int*>(w.part);
+  p.part = reinterpret_cast<float*>(w.part + verify_kv8_plan_bytes());
+  p.wait_limit = g_wait_limit.load();
+  p.num_requests = batch->num_requests;
+  int nl = 0;
+  const int st = launch_verify_kv8(k1, v1, k8, v8, p, c->head_dim, batch->batch, sms, (cudaStream_t)stream, &nl);
+  g_launches.fetch_add((uint64_t)nl, std::memory_order_relaxed);
+  return st;
+}
+
+int s3r_sparse_draft_attn_kv8(const s3r_kv8_cache* cache, const s3r_batch* batch, const int32_t* draft_step,
+                              const void* q, int64_t q_stride, const int32_t* sel_idx, int32_t sel_stride,
+                              const int32_t* sel_count, void* out, float* lse, void* ws, size_t ws_bytes,
+                              s3r_stream_t stream) {
+  S3R_TRY(check_kv8_cache(cache));
+  S3R_TRY(check_batch(batch, true));
+  const s3r_kv_cache* c = &cache->pools;
+  if (!draft_step || !q || !sel_idx || !sel_count || !out || !aligned4(draft_step) || !aligned16(q) ||
+      !aligned4(sel_idx) || !aligned4(sel_count) || !aligned16(out) || (lse && !aligned4(lse)) || sel_stride < 1)
+    return S3R_ERR_INVALID_ARG;
+  const int64_t qrow = (int64_t)c->num_q_heads * c->head_dim;
+  if (q_stride == 0) q_stride = qrow;
+  if (q_stride < qrow || (q_stride % 8)) return S3R_ERR_INVALID_ARG;
+  if (batch->batch == 0) return S3R_OK;
+  const int sms = sm_count();
+  S3R_TRY(check_ws(ws, ws_bytes, head_bytes(batch->num_requests) +
+                                     draft_kv8_bytes(batch->num_requests, c->num_kv_heads, sel_stride, c->head_dim, sms)));
+  const Carve w = carve(ws, batch->num_requests);
+  DraftKv8Params p;
+  std::memset(&p, 0, sizeof(p));
+  p.req_ids = batch->req_ids;
+  p.seq_lens = batch->seq_lens;
+  p.page_table = batch->page_table;
+  p.max_pages = batch->max_pages_per_req;
+  p.cap = batch->max_pages_per_req * S3R_PAGE_SIZE;
+  p.Hq = c->num_q_heads;
+  p.Hkv = c->num_kv_heads;
+  p.G = c->num_q_heads / c->num_kv_heads;
+  p.num_pages = c->num_pages;
+  p.k_pool = static_cast<const uint8_t*>(c->k_pool);
+  p.v_pool = static_cast<const uint8_t*>(c->v_pool);
+  p.k_scale = cache->k_scale;
+  p.v_scale = cache->v_scale;
+  p.draft_step = draft_step;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.q_stride = q_stride;
+  p.sel_idx = sel_idx;
+  p.sel_stride = sel_stride;
+  p.sel_count = sel_count;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.scale = 1.0f / sqrtf((float)c->head_dim);
+  p.err = w.err;
+  p.tickets = w.tickets;
+  p.part = reinterpret_cast<float*>(w.part);
+  p.chunk = draft_kv8_chunk(batch->batch * c->num_kv_heads, sel_stride, sms);
+  p.num_requests = batch->num_requests;
+  return finish(launch_draft_kv8(p, c->head_dim, batch->batch, (cudaStream_t)stream), 1);
+}
+
+size_t s3r_pages_workspace_size(int32_t num_requests) {
+  return num_requests < 0 ? 0 : head_bytes(num_requests > 0 ? num_requests : 1);
+}
+
+static int check_pages(const s3r_batch* b, const int32_t* page_table, const int32_t* held, const int32_t* free_pages,
+                       const int32_t* free_count, int32_t free_capacity, const int32_t* held_out,
+                       const int32_t* free_count_out) {
+  S3R_TRY(check_batch(b, false));
+  if (b->batch > 65535) return S3R_ERR_UNSUPPORTED;
+  if (b->batch == 0) return S3R_OK;
+  if (b->max_pages_per_req <= 0) return S3R_ERR_INVALID_ARG;
+  if ((int64_t)b->max_pages_per_req * S3R_PAGE_SIZE >= ((int64_t)1 << 30)) return S3R_ERR_UNSUPPORTED;
+  for (const int32_t* q : {page_table, held, free_pages, free_count, held_out, free_count_out})
+    if (!q || !aligned4(q)) return S3R_ERR_INVALID_ARG;
+  return free_capacity < 0 ? S3R_ERR_INVALID_ARG : S3R_OK;
+}
+
+static PagesParams pages_params(const s3r_batch* b, int32_t* page_table, const int32_t* held, int32_t* free_pages,
+                                const int32_t* free_count, int32_t free_capacity, int32_t* held_out,
+                                int32_t* free_count_out, const Carve& w) {
+  PagesParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.req_ids = b->req_ids;
+  p.seq_lens = b->seq_lens;
+  p.page_table = page_table;
+  p.max_pages = b->max_pages_per_req;
+  p.batch = b->batch;
+  p.num_requests = b->num_requests;
+  p.held = held;
+  p.free_pages = free_pages;
+  p.free_count = free_count;
+  p.free_capacity = free_capacity;
+  p.held_out = held_out;
+  p.free_count_out = free_count_out;
+  p.err = w.err;
+  p.ticket = w.tickets;
+  return p;
+}
+
+int s3r_alloc_pages(const s3r_batch* batch, int32_t* page_table, int32_t T, const int32_t* n_new,
+                    const int32_t* held, const int32_t* free_pages, const int32_t* free_count,
+                    int32_t free_capacity, int32_t* held_out, int32_t* free_count_out, int32_t* granted,
+                    int64_t* slot_map, void* ws, size_t ws_bytes, s3r_stream_t stream) {
+  S3R_TRY(check_pages(batch, page_table, held, free_pages, free_count, free_capacity, held_out, free_count_out));
+  if (batch->batch == 0) return S3R_OK;
+  if (T < 0 || T >= (1 << 30) || !granted || !aligned4(granted) || (n_new && !aligned4(n_new)) ||
+      (reinterpret_cast<uintptr_t>(slot_map) & 7u))
+    return S3R_ERR_INVALID_ARG;
+  S3R_TRY(check_ws(ws, ws_bytes, s3r_pages_workspace_size(batch->num_requests)));
+  PagesParams p = pages_params(batch, page_table, held, const_cast<int32_t*>(free_pages), free_count, free_capacity,
+                               held_out, free_count_out, carve(ws, batch->num_requests));
+  p.T = T;
+  p.n_new = n_new;
+  p.granted = granted;
+  p.slot_map = slot_map;
+  return finish(launch_alloc_pages(p, (cudaStream_t)stream), 1);
+}
+
+int s3r_release_pages(const s3r_batch* batch, const int32_t* page_table, const int32_t* keep_len,
+                      const int32_t* held, int32_t* free_pages, const int32_t* free_count, int32_t free_capacity,
+                      int32_t* held_out, int32_t* free_count_out, void* ws, size_t ws_bytes, s3r_stream_t stream) {
+  S3R_TRY(check_pages(batch, page_table, held, free_pages, free_count, free_capacity, held_out, free_count_out));
+  if (batch->batch == 0) return S3R_OK;
+  if (keep_len && !aligned4(keep_len)) return S3R_ERR_INVALID_ARG;
+  S3R_TRY(check_ws(ws, ws_bytes, s3r_pages_workspace_size(batch->num_requests)));
+  PagesParams p = pages_params(batch, const_cast<int32_t*>(page_table), held, free_pages, free_count, free_capacity,
+                               held_out, free_count_out, carve(ws, batch->num_requests));
+  p.keep_len = keep_len;
+  return finish(launch_release_pages(p, (cudaStream_t)stream), 1);
 }
 
 int s3r_draft_sample(const s3r_batch* batch, const int32_t* draft_step, int32_t k,

@@ -1,0 +1,1074 @@
+// Dense verify attention over the 8-bit cache (e4m3 codes, one scale per (page, KV head) for
+// K and for V) on the 5th-generation tensor cores, head_dim 64 and 128, up to 64 rows per KV
+// head (padded to NP = 16, 32, 48 or 64).
+//
+// What it computes: row (t, g) of a request at committed length L attends positions 0..L+t of
+//   k_j = K[j] ks[page(j)],  v_j = V[j] vs[page(j)]
+//   x_j = q . k_j / sqrt(d),  out = sum_j softmax(x)_j v_j,  lse = log sum_j exp(x_j)
+// with every committed logit written when asked. The block's own rows are read from the cache
+// (s3r_kv8_append puts them there first).
+//
+// Bound: HBM, 2 d bytes of codes per position and KV head; the score capture adds 4 bytes per
+// row and position. The codes are never converted: both products run as e4m3 x e4m3
+// (kind::f8f6f4, fp32 accumulation) and the bf16 side of each is split in two e4m3 parts:
+//   q 2^-e = qh + ql, qh = e4m3(q 2^-e), ql = e4m3(q 2^-e - qh), the row's largest element
+//     scaled to [128, 256): a bf16 value has 8 significant bits and each part holds 4, so the
+//     split is exact down to 2^-10 of the row's largest element and off by at most 2^-18 of it
+//     below. Both parts accumulate into the same S (8 MMAs of K = 32 per tile at d = 128).
+//   p = 256 2^(x - max) vs / vsmax: ph = e4m3(p), pl = e4m3(16 (p - ph)): within 2^-9 of p
+//     (bf16's half step is 2^-9 of the next power of two) and 2^-14 / 256 of the largest weight
+//     below the normal range. The two parts stand side by side along N (2 NP columns), so a tile
+//     takes 4 MMAs; an MMA of M = 128, K = 32 takes about 70 cycles at N = 32 and at N = 64
+//     alike (measured), so the wider product costs no more.
+// The scales enter in fp32: ks times the logit of its position (one tensor-memory lane = one
+// position = one page), vs into p, relative to the chunk's largest.
+//
+// Organisation: one persistent CTA per SM. A work item is a span of consecutive tiles of 128
+// positions of one (request, KV head); spans are claimed from a counter in the workspace. A span
+// is walked in chunks of up to kMT tiles, whose logits stay in tensor memory for an exact
+// two-pass softmax; the chunks of a span are joined in registers (running max and sum), the
+// spans of a (request, KV head) by a second kernel. The span length follows from the launch's
+// total number of tiles: about 6 spans per CTA when there is much to read, so that the claims
+// balance the SMs while the span records stay a few per cent of the traffic; with little to read,
+// 2 spans per CTA down to single tiles, so that a few long requests use every SM.
+//   warp 0     claims spans, streams K tiles (2 KB per page, one TMA box of 16 KB when the 8
+//              pages of a tile are consecutive), publishes each chunk's page scales
+//   warp 1     streams V tiles, zeroing the rows behind the context's end (0 x NaN is NaN), and
+//              splits each span's q rows into the K-major operand while the span before it streams
+//              (a warp of its own would cost the softmax warps 40 of their 168 registers)
+//   warp 2     issues S^T tile (128 positions x NP) = K . [qh, ql]^T, a ring of kNS tiles in
+//              tensor memory
+//   warp 3     issues O^T (128 d x 2 NP) += V^T . [ph, pl]^T, a ring of kPT tiles of P^T
+//   warps 4-11 softmax, two warpgroups of half the rows each, one thread per position
+// All rings hand over tile by tile. Every wait is bounded (S3R_ERR_TIMEOUT, as in verify_tc.cu).
+#include "kernels.h"
+#include "kv8.cuh"
+#include "tcgen05.cuh"
+
+namespace s3r {
+namespace kv8 {
+
+using namespace tc;
+
+constexpr int kPos = 128;
+constexpr int kThreads = 384;
+constexpr int kSoftWarp0 = 4;
+constexpr int kTileBytes = kPos * 128;    // 16 KB: 128 positions x 128 bytes (d = 64: half zero)
+constexpr int kRing = 16;
+constexpr int kScaleBufs = 4;             // chunks whose page scales are held
+constexpr int kMaxBatch = 256;            // requests per launch (larger batches: several launches)
+// plan area of the workspace (written by the attention kernel for the merge): span length in
+// tiles, then the prefix of per-request span counts
+constexpr int kPlanInts = 512;
+static_assert(kMaxBatch + 2 <= kPlanInts, "plan area");
+
+// Instruction descriptor of kind::f8f6f4: e4m3 A and B, fp32 D.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn, bool b_mn) {
+  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                         uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+template <int NP>
+struct Cfg {
+  // Tensor memory (512 columns): two O buffers of 2 NP columns, then the S ring. A chunk's tiles
+  // must all be resident between the softmax's two passes (kMT <= kNS); what the ring holds
+  // beyond a chunk lets the next chunk's QK run during this chunk's second pass.
+  static constexpr int kOCols = 2 * NP;
+  static constexpr int kSCol0 = 2 * kOCols;
+  static constexpr int kNS = NP == 16 ? 24 : (NP == 32 ? 12 : (NP == 48 ? 6 : 4));
+  static constexpr int kMT = NP <= 32 ? 8 : (NP == 48 ? 5 : 3);   // tiles per chunk
+  static_assert(kSCol0 + kNS * NP <= 512 && kMT <= kNS && kMT <= 8, "tensor memory budget");
+  static constexpr int kPRow = 2 * NP;                            // bytes of P^T per position
+  static constexpr int kPTile = kPos * kPRow;
+  static constexpr int kPT = 4;                                   // P^T ring
+  static constexpr int kKSt = NP <= 32 ? 5 : (NP == 48 ? 4 : 3);  // K ring stages
+  static constexpr int kVSt = NP <= 32 ? 5 : (NP == 48 ? 4 : 3);  // V ring stages
+  // P^T swizzle: 32-byte rows at 16 rows; 64 at 32; 128 at 64; three 32-byte atoms at 48
+  static constexpr uint32_t kPSwz = (NP == 16 || NP == 48) ? 6u : (NP == 32 ? 4u : 2u);
+  static constexpr int kPAtomRow = (NP == 16 || NP == 48) ? 32 : kPRow;   // bytes of one atom's row
+  static constexpr int kPAtomBytes = kPos * kPAtomRow;
+  static constexpr int kQBytes = 2 * NP * 128;                    // one Q buffer: [h, l][NP rows][128 B]
+  static constexpr int kKOff = 0;
+  static constexpr int kVOff = kKSt * kTileBytes;
+  static constexpr int kQOff = kVOff + kVSt * kTileBytes;
+  static constexpr int kPOff = kQOff + 2 * kQBytes;
+  static constexpr int kRedOff = kPOff + kPT * kPTile;
+  // floats: redM, redL [8 warps][NH]; cm, fa, fb, rm, rl [2][NP]; rs [4][NP]; scales [4][2][64]
+  static constexpr int kRedFloats = 2 * 8 * (NP / 2) + 5 * 2 * NP + 4 * NP + kScaleBufs * 128;
+  static constexpr int kPrefOff = kRedOff + kRedFloats * 4;
+  static constexpr int kLenOff = kPrefOff + (kMaxBatch + 4) * 4;
+  static constexpr int kRidOff = kLenOff + kMaxBatch * 4;
+  static constexpr int kIdsOff = kRidOff + kMaxBatch * 4;
+  static constexpr int kBarOff = (kIdsOff + 2 * 64 * 4 + 63) / 64 * 64;
+  static constexpr int kSmem = kBarOff + 1280 + 1024;
+  static_assert(kSmem <= 227 * 1024, "shared memory budget");
+  static_assert(kQOff % 1024 == 0 && kPOff % 1024 == 0 && kRedOff % 16 == 0, "operand alignment");
+};
+
+struct Bars {
+  uint64_t kfull[5], kempty[5], ktma[5];
+  uint64_t vfull[5], vempty[5], vtma[5];
+  uint64_t sfull[24], sempty[24];
+  uint64_t pfull[4], pfree[4];
+  uint64_t q_full[2], q_empty[2];        // per span parity
+  uint64_t qk_done[2], sm_done[2];       // per chunk parity: QK complete; softmax's second pass complete
+  uint64_t sc_full[kScaleBufs];          // chunk's page scales are in shared memory
+  uint64_t o_full[2], o_empty[2];        // per chunk parity
+  uint64_t fin[2];
+  uint64_t wg[2];
+  uint64_t item_bar[kRing];
+  int item_id[kRing];
+  uint32_t tmem_base;
+  int abort_flag;
+  int span;                              // tiles per span of this launch
+};
+static_assert(sizeof(Bars) <= 1280, "barrier block");
+
+// A span of tiles [t0, t1) of (request r, KV head kvh); L committed positions, Lc = L + T.
+struct Span {
+  int id, r, kvh, s, nsp, L, Lc, t0, t1;
+};
+
+__device__ __forceinline__ Span make_span(int id, const int* pref, const int* lens_s, const int* rid_s,
+                                          int batch, int Hkv, int T, int st) {
+  int lo = 0, hi = batch;   // largest b with pref[b] <= id
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pref[mid] <= id) lo = mid;
+    else hi = mid;
+  }
+  Span x;
+  x.id = id;
+  const int rem = id - pref[lo];
+  x.nsp = (pref[lo + 1] - pref[lo]) / Hkv;
+  x.kvh = rem / x.nsp;
+  x.s = rem - x.kvh * x.nsp;
+  x.r = rid_s[lo];
+  x.L = lens_s[lo];
+  x.Lc = x.L + T;
+  x.t0 = x.s * st;
+  x.t1 = min(x.t0 + st, (x.Lc + kPos - 1) / kPos);
+  return x;
+}
+
+// Reduce v[0..N-1] over the warp's lanes with `op`, halving the values at each exchange instead
+// of reducing each one by itself (N = 16: 16 shuffles, not 80). Lane l ends up with the result
+// of column col_of(l), the same one in every lane that shares it.
+template <int N>
+struct ColReduce {
+  static constexpr int NP2 = N <= 8 ? 8 : (N <= 16 ? 16 : 32);   // N = 24 is padded to 32
+  // column that lane l holds after run()
+  __device__ __forceinline__ static int col_of(int lane) {
+    int c = 0;
+#pragma unroll
+    for (int w = NP2 / 2, b = 16; w >= 1; w >>= 1, b >>= 1)
+      if (lane & b) c += w;
+    return c;
+  }
+  template <class Op>
+  __device__ __forceinline__ static float run(const float (&v)[N], int lane, float pad, Op op) {
+    float x[NP2];
+#pragma unroll
+    for (int i = 0; i < NP2; ++i) x[i] = i < N ? v[i] : pad;
+    int b = 16;
+#pragma unroll
+    for (int w = NP2 / 2; w >= 1; w >>= 1) {
+      const bool up = (lane & b) != 0;
+#pragma unroll
+      for (int i = 0; i < w; ++i) {
+        const float send = up ? x[i] : x[i + w];
+        const float keep = up ? x[i + w] : x[i];
+        x[i] = op(keep, __shfl_xor_sync(kFull, send, b));
+      }
+      b >>= 1;
+    }
+    for (; b >= 1; b >>= 1) x[0] = op(x[0], __shfl_xor_sync(kFull, x[0], b));
+    return x[0];
+  }
+};
+
+template <int NP, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    verify_kv8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                      const __grid_constant__ CUtensorMap tmK8, const __grid_constant__ CUtensorMap tmV8,
+                      const VerifyKv8Params p, int batch) {
+  pdl_wait();
+  using C = Cfg<NP>;
+  constexpr int NH = NP / 2;
+  extern __shared__ uint8_t smem_dyn[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
+  float* redM = reinterpret_cast<float*>(smem + C::kRedOff);   // [8][NH]
+  float* redL = redM + 8 * NH;                                  // [8][NH]
+  float* cm = redL + 8 * NH;                                    // [2][NP] chunk max (log2 units)
+  float* fa = cm + 2 * NP;                                      // [2][NP] factor of the running O
+  float* fb = fa + 2 * NP;                                      // [2][NP] factor of the chunk's O
+  float* rm = fb + 2 * NP;                                      // [2][NP] running max
+  float* rl = rm + 2 * NP;                                      // [2][NP] running sum
+  float* rs = rl + 2 * NP;                                      // [4][NP] q row factor 2^e / sqrt(d)
+  float* scs = rs + 4 * NP;                                     // [4][2][64] page scales (ks, vs)
+  int* pref = reinterpret_cast<int*>(smem + C::kPrefOff);
+  int* lens_s = reinterpret_cast<int*>(smem + C::kLenOff);
+  int* rid_s = reinterpret_cast<int*>(smem + C::kRidOff);
+  int* ids_s = reinterpret_cast<int*>(smem + C::kIdsOff);
+  Bars* B = reinterpret_cast<Bars*>(smem + C::kBarOff);
+  volatile int* abort_flag = &B->abort_flag;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int T = p.T, G = p.G, R = p.R, Hkv = p.Hkv;
+  const uint32_t sbase = smem_u32(smem);
+
+  // ---- set-up: lengths, span length, span prefix, barriers, tensor memory
+  for (int b = tid; b < batch; b += blockDim.x) {
+    const int r = p.req_ids ? p.req_ids[p.req_off + b] : p.req_off + b;
+    const bool known = r >= 0 && r < p.num_requests;
+    const int L = known ? p.seq_lens[r] : -1;
+    const bool fits = L >= 0 && L <= p.cap - T;
+    if (!fits && blockIdx.x == 0) set_error(p.err, S3R_ERR_DEVICE_BOUNDS);
+    rid_s[b] = known ? r : 0;
+    lens_s[b] = L;
+    pref[b + 1] = fits ? (L + T + kPos - 1) / kPos : 0;   // tiles, turned into span counts below
+  }
+  if (tid == 0) {
+    for (int s = 0; s < C::kKSt; ++s) {
+      mbar_init(smem_u32(&B->kfull[s]), 1);
+      mbar_init(smem_u32(&B->kempty[s]), 1);
+      mbar_init(smem_u32(&B->ktma[s]), 1);
+    }
+    for (int s = 0; s < C::kVSt; ++s) {
+      mbar_init(smem_u32(&B->vfull[s]), 1);
+      mbar_init(smem_u32(&B->vempty[s]), 1);
+      mbar_init(smem_u32(&B->vtma[s]), 1);
+    }
+    for (int s = 0; s < C::kNS; ++s) {
+      mbar_init(smem_u32(&B->sfull[s]), 1);
+      mbar_init(smem_u32(&B->sempty[s]), 8);
+    }
+    for (int s = 0; s < C::kPT; ++s) {
+      mbar_init(smem_u32(&B->pfull[s]), 8);
+      mbar_init(smem_u32(&B->pfree[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&B->q_full[b]), 1);
+      mbar_init(smem_u32(&B->q_empty[b]), 1);
+      mbar_init(smem_u32(&B->qk_done[b]), 1);
+      mbar_init(smem_u32(&B->sm_done[b]), 8);
+      mbar_init(smem_u32(&B->o_full[b]), 1);
+      mbar_init(smem_u32(&B->o_empty[b]), 8);
+      mbar_init(smem_u32(&B->fin[b]), 1);
+      mbar_init(smem_u32(&B->wg[b]), 4);
+    }
+    for (int i = 0; i < kScaleBufs; ++i) mbar_init(smem_u32(&B->sc_full[i]), 1);
+    for (int i = 0; i < kRing; ++i) mbar_init(smem_u32(&B->item_bar[i]), 1);
+    B->abort_flag = 0;
+    fence_mbar_init();
+    fence_proxy_async();
+  }
+  if (warp == 2) {
+    tmem_alloc(smem_u32(&B->tmem_base), 512);
+    tmem_relinquish();
+  }
+  __syncthreads();
+  if (warp == 0) {
+    const int per = (batch + 31) / 32;
+    const int b0 = lane * per, b1 = min(batch, b0 + per);
+    long long tiles = 0;
+    for (int b = b0; b < b1; ++b) tiles += pref[b + 1];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) tiles += __shfl_xor_sync(kFull, tiles, o);
+    const int st = span_tiles(tiles * Hkv, (int)gridDim.x, C::kMT);
+    int local = 0;
+    for (int b = b0; b < b1; ++b) local += Hkv * ((pref[b + 1] + st - 1) / st);
+    int incl = local;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += v;
+    }
+    int run = incl - local;
+    for (int b = b0; b < b1; ++b) {
+      run += Hkv * ((pref[b + 1] + st - 1) / st);
+      pref[b + 1] = run;
+    }
+    if (lane == 0) {
+      pref[0] = 0;
+      B->span = st;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = B->tmem_base;
+  const int nitems = pref[batch], st = B->span;
+  if (blockIdx.x == 0)   // the merge's plan
+    for (int b = tid; b <= batch + 1; b += blockDim.x) p.plan[b] = b == 0 ? st : pref[b - 1];
+
+  // A CTA's first span is blockIdx.x, later ones come from the launch's counter; the K producer
+  // claims them and publishes the ids in a ring (id >= nitems: no more work).
+  auto ring_id = [&](int m) -> int {   // warp-uniform; -1 if the wait gave up
+    const int slot = m & (kRing - 1);
+    if (!wait_bar(smem_u32(&B->item_bar[slot]), (uint32_t)(m / kRing) & 1u, abort_flag, p.err, p.wait_limit)) return -1;
+    return *reinterpret_cast<volatile int*>(&B->item_id[slot]);
+  };
+  auto span_of = [&](int id) { return make_span(id, pref, lens_s, rid_s, batch, Hkv, T, st); };
+  auto waitb = [&](uint64_t* bar, int phase) -> bool {
+    return wait_bar(smem_u32(bar), (uint32_t)phase & 1u, abort_flag, p.err, p.wait_limit);
+  };
+  const uint32_t qbuf = sbase + C::kQOff, pbuf = sbase + C::kPOff;
+
+  if (warp <= 1) {
+    // ============================================================ producers ====
+    const bool is_v = warp == 1;
+    const CUtensorMap* map = is_v ? &tmV : &tmK;
+    const CUtensorMap* map8 = is_v ? &tmV8 : &tmK8;
+    if (lane == 0) {
+      asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+      asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(map8)) : "memory");
+    }
+    const int nst = is_v ? C::kVSt : C::kKSt;
+    const int roff = is_v ? C::kVOff : C::kKOff;
+    uint64_t* full = is_v ? B->vfull : B->kfull;
+    uint64_t* empty = is_v ? B->vempty : B->kempty;
+    uint64_t* tmab = is_v ? B->vtma : B->ktma;
+    int* ids_own = ids_s + (is_v ? 64 : 0);
+    int g = 0;                 // tiles issued
+    uint32_t tma_phase = 0;    // bit s: phase of tmab[s]
+    bool stop = false;
+    // Page ids of the chunk [t0, t1), two per lane (-1 past the context or outside the pool).
+    auto fetch_ids = [&](const Span& x, int t0, int t1, int& a, int& b) {
+      const int* ptab = p.page_table + (size_t)x.r * p.max_pages;
+      const int npg = (t1 - t0) * 8, pg0 = t0 * 8, pend = (x.Lc + kPage - 1) / kPage;
+      a = lane < npg && pg0 + lane < pend ? ptab[pg0 + lane] : -1;
+      b = lane + 32 < npg && pg0 + lane + 32 < pend ? ptab[pg0 + lane + 32] : -1;
+    };
+    auto load_tile = [&](const Span& x, int t, int i0) {   // i0: the tile's first page in ids_own
+      const int s = g % nst;
+      if (g >= nst && !waitb(&empty[s], g / nst - 1)) {
+        stop = true;
+        return;
+      }
+      const uint32_t dst = sbase + roff + s * kTileBytes;
+      const int pend = (x.Lc + kPage - 1) / kPage;
+      // one page per lane (lanes 0..7)
+      const int pg = t * 8 + lane;
+      const int id = lane < 8 ? ids_own[i0 + lane] : -1;
+      const bool want = lane < 8 && pg < pend;
+      const bool good = want && id >= 0 && id < p.num_pages;
+      if (want && !good) set_error(p.err, S3R_ERR_DEVICE_BOUNDS);
+      const uint32_t okmask = __ballot_sync(kFull, good) & 0xFFu;
+      const uint32_t wantmask = __ballot_sync(kFull, want) & 0xFFu;
+      const int id0 = __shfl_sync(kFull, id, 0);
+      const bool run = __all_sync(kFull, lane >= 8 || (good && id == id0 + lane));
+      // rows that must read as zero: a bad page's, and for V every row behind the context
+      const bool patch = okmask != wantmask || (is_v && (t + 1) * kPos > x.Lc);
+      const uint32_t landing = smem_u32(patch ? &tmab[s] : &full[s]);
+      if (lane == 0) mbar_arrive_expect_tx(landing, (uint32_t)__popc(okmask) * kPage * 128);
+      __syncwarp();
+      if (run) {
+        if (lane == 0) tma_load_4d(dst, map8, 0, 0, x.kvh, id0, landing);
+      } else if (good) {
+        tma_load_4d(dst + lane * kPage * 128, map, 0, 0, x.kvh, id, landing);
+      }
+      ++g;
+      if (patch) {
+        if (!waitb(&tmab[s], (tma_phase >> s) & 1)) {
+          mbar_wait(smem_u32(&tmab[s]), (tma_phase >> s) & 1);   // its copies land before exit
+          if (lane == 0) mbar_arrive(smem_u32(&full[s]));        // (for the wait below)
+          stop = true;
+          return;
+        }
+        tma_phase ^= 1u << s;
+        for (int idx = lane; idx < kPos * 8; idx += 32) {
+          const int row = idx >> 3;
+          if ((okmask & (1u << (row >> 4))) && !(is_v && t * kPos + row >= x.Lc)) continue;
+          *reinterpret_cast<uint4*>(smem + roff + s * kTileBytes + idx * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&full[s]));
+      }
+      __syncwarp();
+    };
+    auto item_id = [&](int m) -> int {
+      if (is_v) return ring_id(m);
+      int id = (int)blockIdx.x;
+      if (m > 0) {
+        int v = 0;
+        if (lane == 0) v = atomicAdd(p.sched, 1);
+        id = __shfl_sync(kFull, v, 0) + (int)gridDim.x;
+      }
+      id = min(id, nitems);
+      if (lane == 0) {
+        B->item_id[m & (kRing - 1)] = id;
+        mbar_arrive(smem_u32(&B->item_bar[m & (kRing - 1)]));   // release: the id is visible
+      }
+      __syncwarp();
+      return id;
+    };
+    // q rows of span m -> buffer m & 1 (V producer), once the QK of span m - 2 has read it
+    constexpr int LR = D / 8;          // lanes per row (8 elements each)
+    constexpr int RI = 32 / LR;        // rows per pass
+    auto zero_q_padding = [&]() {   // rows R..NP-1 of both parts of both buffers stay zero
+      for (int idx = lane; idx < 4 * (NP - R) * 8; idx += 32) {
+        const int h = idx / ((NP - R) * 8), rem = idx - h * (NP - R) * 8;   // h: buffer * 2 + part
+        *reinterpret_cast<uint4*>(smem + C::kQOff + h * (NP * 128) + (R + (rem >> 3)) * 128 + ((rem & 7) << 4)) =
+            make_uint4(0, 0, 0, 0);
+      }
+    };
+    auto split_q = [&](const Span& x, int m) -> bool {
+      const int qb = m & 1;
+      if (m >= 2 && !waitb(&B->q_empty[qb], (m - 2) >> 1)) return false;
+      for (int j0 = 0; j0 < R; j0 += RI) {
+        const int j = j0 + lane / LR, c8 = lane % LR;
+        uint4 raw = make_uint4(0, 0, 0, 0);
+        if (j < R) {
+          const int t = j / G, gq = j - t * G;
+          raw = *reinterpret_cast<const uint4*>(p.q + (((size_t)x.r * T + t) * p.Hq + x.kvh * G + gq) * D + c8 * 8);
+        }
+        // largest |q| of the row by its bits (NaN above infinity above every finite value)
+        uint32_t a = __vmaxu2(__vmaxu2(raw.x & 0x7fff7fffu, raw.y & 0x7fff7fffu),
+                              __vmaxu2(raw.z & 0x7fff7fffu, raw.w & 0x7fff7fffu));
+        uint32_t amax = max(a & 0xffffu, a >> 16);
+#pragma unroll
+        for (int o = LR / 2; o; o >>= 1) amax = max(amax, __shfl_xor_sync(kFull, amax, o));
+        // the largest element's exponent goes to 2^7; a row of tiny values is not scaled past 2^120
+        const int e = max((int)(amax >> 7) - 127 - 7, -120);
+        const bool bad = amax >= 0x7f80u;   // NaN or infinity: the row's logits become NaN
+        const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+        uint32_t hi[2], lo[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t hh = 0, ll = 0;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const uint32_t v = w[2 * i + u];
+            const float f0 = __uint_as_float(v << 16) * inv, f1 = __uint_as_float(v & 0xffff0000u) * inv;
+            const uint32_t h2 = pack_e4m3(f0, f1);
+            const float2 hf = unpack_e4m3(h2);
+            const uint32_t l2 = pack_e4m3(f0 - hf.x, f1 - hf.y);
+            hh |= h2 << (16 * u);
+            ll |= l2 << (16 * u);
+          }
+          hi[i] = bad ? 0x7f7f7f7fu : hh;
+          lo[i] = bad ? 0x7f7f7f7fu : ll;
+        }
+        if (j < R) {
+          uint8_t* dst = smem + C::kQOff + qb * C::kQBytes + j * 128 + (((c8 >> 1) ^ (j & 7)) << 4) + (c8 & 1) * 8;
+          *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
+          *reinterpret_cast<uint2*>(dst + NP * 128) = make_uint2(lo[0], lo[1]);
+          if (c8 == 0) {
+            rs[(m & 3) * NP + j] = __uint_as_float((uint32_t)(127 + e) << 23) * p.scale;
+            if (bad) set_error(p.err, S3R_ERR_NONFINITE);
+          }
+        }
+      }
+      for (int j = R + lane; j < NP; j += 32) rs[(m & 3) * NP + j] = 0.f;
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&B->q_full[qb]));
+      return true;
+    };
+    // The chunk after (x, t0): the next of the span, or the first of the next span.
+    int m = 0, n = 0;   // span and chunk counters
+    int cur = item_id(0);
+    Span x{};
+    int t0 = 0, t1 = 0, ida = -1, idb = -1;
+    if (cur >= 0 && cur < nitems) {
+      x = span_of(cur);
+      t0 = x.t0;
+      t1 = min(t0 + C::kMT, x.t1);
+      fetch_ids(x, t0, t1, ida, idb);
+      if (is_v) {
+        zero_q_padding();
+        if (!split_q(x, 0)) stop = true;
+      }
+    }
+    while (cur >= 0 && cur < nitems && !stop && !aborted(abort_flag)) {
+      __syncwarp();
+      ids_own[lane] = ida;
+      ids_own[lane + 32] = idb;
+      __syncwarp();
+      // page scales of this chunk (K producer): loaded now, stored once the first tile is issued
+      float ka = 0.f, kb = 0.f, va = 0.f, vb = 0.f;
+      if (!is_v) {
+        if (ida >= 0 && ida < p.num_pages) {
+          ka = __ldg(p.k_scale + (size_t)ida * Hkv + x.kvh);
+          va = __ldg(p.v_scale + (size_t)ida * Hkv + x.kvh);
+        }
+        if (idb >= 0 && idb < p.num_pages) {
+          kb = __ldg(p.k_scale + (size_t)idb * Hkv + x.kvh);
+          vb = __ldg(p.v_scale + (size_t)idb * Hkv + x.kvh);
+        }
+      }
+      // At most two chunks ahead of QK, checked before this chunk's first tile (QK(n) cannot be
+      // over yet): scale buffer n & 3 was read by chunk n - 4, whose softmax is over once QK(n - 2) is.
+      if (!is_v && n >= 2 && !waitb(&B->qk_done[n & 1], (n - 2) >> 1)) break;
+      load_tile(x, t0, 0);
+      if (stop) break;
+      if (!is_v) {
+        float* sc = scs + (n & (kScaleBufs - 1)) * 128;
+        sc[lane] = good_scale(ka, p.err);
+        sc[lane + 32] = good_scale(kb, p.err);
+        sc[64 + lane] = good_scale(va, p.err);
+        sc[64 + lane + 32] = good_scale(vb, p.err);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&B->sc_full[n & (kScaleBufs - 1)]));
+      }
+      // what comes next is claimed and its page ids are fetched while this chunk streams
+      int nt0 = t1, nt1, na, nb, nxt = cur;
+      Span xn = x;
+      if (t1 >= x.t1) {
+        nxt = item_id(++m);
+        if (nxt >= 0 && nxt < nitems) {
+          xn = span_of(nxt);
+          nt0 = xn.t0;
+        }
+      }
+      nt1 = min(nt0 + C::kMT, xn.t1);
+      na = nb = -1;
+      if (nxt >= 0 && nxt < nitems) {
+        fetch_ids(xn, nt0, nt1, na, nb);
+        if (is_v && t1 >= x.t1 && !split_q(xn, m)) stop = true;
+      }
+      for (int t = t0 + 1; t < t1 && !stop; ++t) load_tile(x, t, (t - t0) * 8);
+      cur = nxt;
+      x = xn;
+      t0 = nt0;
+      t1 = nt1;
+      ida = na;
+      idb = nb;
+      ++n;
+    }
+    // nothing may still be landing in this ring when the CTA exits, also after an abort
+    for (int q = g - nst > 0 ? g - nst : 0; q < g; ++q) mbar_wait(smem_u32(&full[q % nst]), (q / nst) & 1);
+  } else if (warp == 2) {
+    // ===================================================================== QK issuer ====
+    constexpr uint32_t kId = idesc_e4m3(kPos, NP, false, false);
+    int gk = 0, n = 0;
+    bool ok = true;
+    for (int m = 0; ok; ++m) {
+      const int id = ring_id(m);
+      if (id < 0 || id >= nitems) break;
+      const Span x = span_of(id);
+      if (!waitb(&B->q_full[m & 1], m >> 1)) break;
+      for (int t0 = x.t0; t0 < x.t1 && ok; t0 += C::kMT, ++n) {
+        // at most two chunks ahead of the softmax (per-chunk buffers)
+        if (n >= 2 && !waitb(&B->sm_done[n & 1], (n - 2) >> 1)) {
+          ok = false;
+          break;
+        }
+        const int t1 = min(t0 + C::kMT, x.t1);
+        for (int t = t0; t < t1; ++t, ++gk) {
+          const int s = gk % C::kKSt, d = gk % C::kNS;
+          if (!waitb(&B->kfull[s], gk / C::kKSt) || (gk >= C::kNS && !waitb(&B->sempty[d], gk / C::kNS - 1))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t kt = sbase + C::kKOff + s * kTileBytes;
+            const uint32_t qt = qbuf + (m & 1) * C::kQBytes;
+            const uint32_t sd = tmem + C::kSCol0 + d * NP;
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+              for (int kk = 0; kk < D / 32; ++kk)
+                mma_e4m3(sd, sdesc(kt + kk * 32, 16, 1024, 2), sdesc(qt + half * (NP * 128) + kk * 32, 16, 1024, 2),
+                         kId, half + kk > 0 ? 1u : 0u);
+            tc_commit(smem_u32(&B->kempty[s]));
+            tc_commit(smem_u32(&B->sfull[d]));
+          }
+          __syncwarp();
+        }
+        if (ok && lane == 0) tc_commit(smem_u32(&B->qk_done[n & 1]));
+        __syncwarp();
+      }
+      if (ok && lane == 0) tc_commit(smem_u32(&B->q_empty[m & 1]));
+      __syncwarp();
+    }
+    if (lane == 0) tc_commit(smem_u32(&B->fin[0]));
+    __syncwarp();
+    mbar_wait(smem_u32(&B->fin[0]), 0);   // not cut short by an abort: the work is in flight
+  } else if (warp == 3) {
+    // ===================================================================== PV issuer ====
+    constexpr uint32_t kId = idesc_e4m3(kPos, 2 * NP, true, true);
+    int gv = 0, n = 0;
+    bool ok = true;
+    for (int m = 0; ok; ++m) {
+      const int id = ring_id(m);
+      if (id < 0 || id >= nitems) break;
+      const Span x = span_of(id);
+      for (int t0 = x.t0; t0 < x.t1 && ok; t0 += C::kMT, ++n) {
+        if (n >= 2 && !waitb(&B->o_empty[n & 1], (n - 2) >> 1)) {
+          ok = false;
+          break;
+        }
+        const int t1 = min(t0 + C::kMT, x.t1);
+        for (int t = t0; t < t1; ++t, ++gv) {
+          const int s = gv % C::kVSt, u = gv % C::kPT;
+          if (!waitb(&B->pfull[u], gv / C::kPT) || !waitb(&B->vfull[s], gv / C::kVSt)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t vt = sbase + C::kVOff + s * kTileBytes;
+            const uint32_t pt = pbuf + u * C::kPTile;
+            const uint32_t od = tmem + (n & 1) * C::kOCols;
+#pragma unroll
+            for (int kk = 0; kk < kPos / 32; ++kk)
+              // MN-major operands: strides between atoms along M / N and between groups of 8 positions
+              mma_e4m3(od, sdesc(vt + kk * 32 * 128, kTileBytes, 1024, 2),
+                       sdesc(pt + kk * 32 * C::kPAtomRow, C::kPAtomBytes, 8 * C::kPAtomRow, C::kPSwz), kId,
+                       t > t0 || kk > 0 ? 1u : 0u);
+            tc_commit(smem_u32(&B->vempty[s]));
+            tc_commit(smem_u32(&B->pfree[u]));
+          }
+          __syncwarp();
+        }
+        if (ok && lane == 0) tc_commit(smem_u32(&B->o_full[n & 1]));
+        __syncwarp();
+      }
+    }
+    if (lane == 0) tc_commit(smem_u32(&B->fin[1]));
+    __syncwarp();
+    mbar_wait(smem_u32(&B->fin[1]), 0);
+  } else {
+    // ================================================================ softmax warps ====
+    const int sg = (warp - kSoftWarp0) >> 2;        // warpgroup: rows [sg NH, sg NH + NH)
+    const int q4 = warp & 3;                        // tensor-memory lane quarter
+    const int gt = (tid - 32 * kSoftWarp0) & 127;   // thread within the warpgroup
+    const int lrow = q4 * 32 + lane;                // tile position (S) or d (O) of this thread
+    const int c0 = sg * NH;
+    const bool lead8 = (c0 & 15) == 8;
+    const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16);
+    // 16-byte chunk XOR of this position's P^T row (32-, 64-, 128-byte swizzle)
+    const int swz_row = (NP == 16 || NP == 48) ? ((lrow >> 2) & 1) : (NP == 32 ? ((lrow >> 1) & 3) : (lrow & 7));
+    uint32_t wg_phase = 0;
+    auto wg_sync = [&]() -> bool {   // bounded, unlike bar.sync
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&B->wg[sg]));
+      const bool r = wait_bar(smem_u32(&B->wg[sg]), wg_phase, abort_flag, p.err, p.wait_limit);
+      wg_phase ^= 1u;
+      return r;
+    };
+    float orun[NH];   // running O of the span (this thread's d), relative to the running max
+    // Chunk n's O joins the span; with its last chunk the span's record (or, when the span is the
+    // whole context, the output) is written.
+    auto epilogue = [&](int n, const Span& x, bool first, bool last) -> bool {
+      if (!waitb(&B->o_full[n & 1], n >> 1)) return false;
+      tc_fence_after();
+      const float* fan = fa + (n & 1) * NP + c0;
+      const float* fbn = fb + (n & 1) * NP + c0;
+      float o[NP];
+      tmem_ld<NP>(tl + (n & 1) * C::kOCols + sg * NP, o);
+      tmem_wait_ld();
+#pragma unroll
+      for (int j = 0; j < NH; ++j) {
+        const float v = fmaf(o[NH + j], 0.0625f, o[j]) * fbn[j];
+        orun[j] = first ? v : fmaf(orun[j], fan[j], v);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&B->o_empty[n & 1]));
+      if (!last) return true;
+      const float* rmn = rm + (n & 1) * NP + c0;
+      const float* rln = rl + (n & 1) * NP + c0;
+      if (x.nsp == 1) {
+        if (lrow < D) {
+#pragma unroll
+          for (int j = 0; j < NH; ++j) {
+            const int row = c0 + j;
+            if (row < R) {
+              const int t = row / G, gq = row - t * G;
+              p.out[(((size_t)x.r * T + t) * p.Hq + x.kvh * G + gq) * D + lrow] = __float2bfloat16_rn(orun[j] / rln[j]);
+            }
+          }
+        }
+        if (gt < NH && c0 + gt < R) {
+          const int row = c0 + gt, t = row / G, gq = row - t * G;
+          p.lse[((size_t)x.r * T + t) * p.Hq + x.kvh * G + gq] = (rmn[gt] + log2f(rln[gt])) * kLn2;
+        }
+        return true;
+      }
+      float* rec = p.part + (size_t)x.id * p.Rp * (D + 2);
+      if (lrow < D) {
+#pragma unroll
+        for (int j = 0; j < NH; ++j)
+          if (c0 + j < R) rec[2 * p.Rp + (size_t)(c0 + j) * D + lrow] = orun[j];
+      }
+      if (gt < NH && c0 + gt < R) {
+        rec[c0 + gt] = rmn[gt];
+        rec[p.Rp + c0 + gt] = rln[gt];
+      }
+      return true;
+    };
+
+    bool ok = true;
+    int n = 0, gs = 0;          // chunk and tile counters
+    float mrun = 0.f, lrun = 0.f;   // of row c0 + gt (threads gt < NH)
+    Span xp{};
+    bool pfirst = false, plast = false;
+    for (int m = 0; ok && !aborted(abort_flag); ++m) {
+      const int id = ring_id(m);
+      if (id < 0) ok = false;
+      if (id < 0 || id >= nitems) break;
+      const Span x = span_of(id);
+      const int L = x.L, Lc = x.Lc;
+      float* scores = p.scores ? p.scores + ((size_t)x.r * Hkv + x.kvh) * (size_t)R * p.cap : nullptr;
+      const float* rsm = rs + (m & 3) * NP + c0;
+      for (int t0 = x.t0; t0 < x.t1 && ok; t0 += C::kMT, ++n) {
+        const int t1 = min(t0 + C::kMT, x.t1), nt = t1 - t0;
+        const bool first = t0 == x.t0, last = t1 == x.t1;
+        if (!waitb(&B->sc_full[n & (kScaleBufs - 1)], n / kScaleBufs)) {
+          ok = false;
+          break;
+        }
+        const float* ksc = scs + (n & (kScaleBufs - 1)) * 128;
+        const float* vsc = ksc + 64;
+        const float vmax = warp_max(fmaxf(vsc[lane], vsc[lane + 32]));
+        const float vnorm = vmax > 0.f ? 256.f / vmax : 0.f;   // a scale under 2^-118 counts as zero
+
+        // pass 1: committed logits out, row maxima (of acc * ks: the row factor is positive)
+        float mrow[NH];
+#pragma unroll
+        for (int j = 0; j < NH; ++j) mrow[j] = -INFINITY;
+        for (int u = 0; u < nt; ++u) {
+          const int d = (gs + u) % C::kNS;
+          if (!waitb(&B->sfull[d], (gs + u) / C::kNS)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          float v[NH];
+          tmem_ld_cols<NH>(tl + C::kSCol0 + d * NP + c0, v, lead8);
+          tmem_wait_ld();
+          const int p0 = (t0 + u) * kPos, pos = p0 + lrow;
+          const float ks = ksc[u * 8 + (lrow >> 4)];
+#pragma unroll
+          for (int j = 0; j < NH; ++j) v[j] *= ks;
+          if (scores && pos < L) {
+            float* srow = scores + (size_t)c0 * p.cap + pos;
+#pragma unroll
+            for (int j = 0; j < NH; ++j)
+              if (c0 + j < R) srow[(size_t)j * p.cap] = v[j] * rsm[j];
+          }
+          if (p0 + kPos <= L) {
+#pragma unroll
+            for (int j = 0; j < NH; ++j) mrow[j] = fmaxf(mrow[j], v[j]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < NH; ++j) {
+              const int row = c0 + j;
+              if (pos < Lc && row < R && (pos < L || (pos - L) * G <= row)) mrow[j] = fmaxf(mrow[j], v[j]);
+            }
+          }
+        }
+        if (!ok) break;
+        {
+          const float r = ColReduce<NH>::run(mrow, lane, -INFINITY, [](float a, float b) { return fmaxf(a, b); });
+          const int c = ColReduce<NH>::col_of(lane);
+          if (c < NH) redM[(sg * 4 + q4) * NH + c] = r;
+        }
+        if (!wg_sync()) {
+          ok = false;
+          break;
+        }
+        float mc = -INFINITY;
+        if (gt < NH) {
+#pragma unroll
+          for (int w = 0; w < 4; ++w) mc = fmaxf(mc, redM[(sg * 4 + w) * NH + gt]);
+          mc *= rsm[gt] * kLog2e;
+          if (c0 + gt >= R) mc = 0.f;
+          cm[(n & 1) * NP + c0 + gt] = mc;
+        }
+        if (!wg_sync()) {
+          ok = false;
+          break;
+        }
+        // row maxima and factors: registers up to 16 rows, beyond that re-read from shared memory
+        // tile by tile (24 and 32 rows spill otherwise)
+        constexpr bool kHeld = NH <= 16;
+        const float* cmn = cm + (n & 1) * NP + c0;
+        float rs2[kHeld ? NH : 1], lsum[NH];
+#pragma unroll
+        for (int j = 0; j < NH; ++j) {
+          if constexpr (kHeld) {
+            mrow[j] = cmn[j];
+            rs2[j] = rsm[j] * kLog2e;
+          }
+          lsum[j] = 0.f;
+        }
+
+        // pass 2: p = 2^(x - max); its sum in fp32, 256 p vs / vsmax in two e4m3 parts to P^T
+        for (int u = 0; u < nt; ++u) {
+          const int d = (gs + u) % C::kNS;
+          float v[NH];
+          tmem_ld_cols<NH>(tl + C::kSCol0 + d * NP + c0, v, lead8);
+          tmem_wait_ld();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&B->sempty[d]));
+          const int p0 = (t0 + u) * kPos, pos = p0 + lrow;
+          const float ks = ksc[u * 8 + (lrow >> 4)];
+          const float vw = vsc[u * 8 + (lrow >> 4)] * vnorm;
+          const bool interior = p0 + kPos <= L;
+          uint32_t hb[NH / 4], lb[NH / 4];
+#pragma unroll
+          for (int j = 0; j < NH; j += 4) {
+            float e[4], mj[4], rj[4];
+            if constexpr (kHeld) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                mj[i] = mrow[j + i];
+                rj[i] = rs2[j + i];
+              }
+            } else {
+              const float4 m4 = *reinterpret_cast<const float4*>(cmn + j);
+              const float4 r4 = *reinterpret_cast<const float4*>(rsm + j);
+              mj[0] = m4.x; mj[1] = m4.y; mj[2] = m4.z; mj[3] = m4.w;
+              rj[0] = r4.x * kLog2e; rj[1] = r4.y * kLog2e; rj[2] = r4.z * kLog2e; rj[3] = r4.w * kLog2e;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              e[i] = ex2(fmaf(v[j + i] * ks, rj[i], -mj[i]));
+              if (!interior) {
+                const int row = c0 + j + i;
+                const bool vis = pos < Lc && row < R && (pos < L || (pos - L) * G <= row) && mj[i] != -INFINITY;
+                e[i] = vis ? e[i] : 0.f;
+              }
+              lsum[j + i] += e[i];
+              e[i] *= vw;
+            }
+            split_e4m3x4(e, hb[j / 4], lb[j / 4]);
+          }
+          const int gp = gs + u, slot = gp % C::kPT;
+          if (gp >= C::kPT && !waitb(&B->pfree[slot], gp / C::kPT - 1)) {
+            ok = false;
+            break;
+          }
+          // this warpgroup's NP bytes of the position's row: NH bytes of ph, then NH of pl
+          uint8_t* ptile = smem + C::kPOff + slot * C::kPTile + lrow * C::kPAtomRow;
+          constexpr int CPA = C::kPAtomRow / 16;
+          if constexpr (NP == 16) {
+            *reinterpret_cast<uint4*>(ptile + ((sg ^ swz_row) << 4)) = make_uint4(hb[0], hb[1], lb[0], lb[1]);
+          } else {
+            uint32_t all[NP / 4];
+#pragma unroll
+            for (int i = 0; i < NH / 4; ++i) {
+              all[i] = hb[i];
+              all[NH / 4 + i] = lb[i];
+            }
+#pragma unroll
+            for (int i = 0; i < NP / 16; ++i) {
+              const int cc = sg * (NP / 16) + i;
+              *reinterpret_cast<uint4*>(ptile + (cc / CPA) * C::kPAtomBytes + (((cc % CPA) ^ swz_row) << 4)) =
+                  make_uint4(all[4 * i], all[4 * i + 1], all[4 * i + 2], all[4 * i + 3]);
+            }
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&B->pfull[slot]));
+        }
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(smem_u32(&B->sm_done[n & 1]));
+        gs += nt;
+        // the previous chunk's O (its PV has had this chunk's passes to finish)
+        if (n > 0 && !epilogue(n - 1, xp, pfirst, plast)) {
+          ok = false;
+          break;
+        }
+        {
+          const float r = ColReduce<NH>::run(lsum, lane, 0.f, [](float a, float b) { return a + b; });
+          const int c = ColReduce<NH>::col_of(lane);
+          if (c < NH) redL[(sg * 4 + q4) * NH + c] = r;
+        }
+        if (!wg_sync()) {
+          ok = false;
+          break;
+        }
+        if (gt < NH) {
+          float l = 0.f;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) l += redL[(sg * 4 + w) * NH + gt];
+          const float ov = vmax * (1.f / 256.f);
+          float a = 0.f, b = ov;
+          if (first) {
+            mrun = mc;
+            lrun = l;
+          } else {
+            const float mn = fmaxf(mrun, mc);
+            a = mrun == -INFINITY ? 0.f : exp2f(mrun - mn);
+            const float bb = mc == -INFINITY ? 0.f : exp2f(mc - mn);
+            b = bb * ov;
+            lrun = lrun * a + l * bb;
+            mrun = mn;
+          }
+          const int k = (n & 1) * NP + c0 + gt;
+          fa[k] = a;
+          fb[k] = b;
+          rm[k] = mrun;
+          rl[k] = lrun;
+        }
+        // (visible to the group at the next chunk's barriers, before the epilogue that reads them)
+        xp = x;
+        pfirst = first;
+        plast = last;
+      }
+    }
+    if (ok && n > 0 && !aborted(abort_flag)) {
+      if (wg_sync()) epilogue(n - 1, xp, pfirst, plast);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  // the last CTA out returns the counters to zero for the next launch
+  if (tid == 0) {
+    __threadfence();
+    if (atomicAdd(p.sched + 1, 1) == (int)gridDim.x - 1) {
+      p.sched[0] = 0;
+      p.sched[1] = 0;
+    }
+  }
+}
+
+// Joins the span records of every (request, KV head) that has more than one: a warp per row,
+// out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s, spans in order (nothing depends on which
+// CTA finished first). The records were just written, so they come from L2.
+constexpr int kMergeWarps = 4;
+template <int D>
+__global__ void __launch_bounds__(32 * kMergeWarps) merge_kv8_kernel(const VerifyKv8Params p, int batch) {
+  pdl_wait();
+  constexpr int V = D / 32;   // consecutive d of a lane
+  const int lane = threadIdx.x & 31;
+  const int row = blockIdx.x * kMergeWarps + (threadIdx.x >> 5), kvh = blockIdx.y, bl = blockIdx.z;
+  if (row >= p.R) return;
+  const int r = p.req_ids ? p.req_ids[p.req_off + bl] : p.req_off + bl;
+  if (r < 0 || r >= p.num_requests) return;      // reported by the attention kernel
+  const int b0 = p.plan[1 + bl], b1 = p.plan[2 + bl];
+  const int nsp = (b1 - b0) / p.Hkv;
+  if (nsp <= 1) return;                          // no work, or written by the attention kernel
+  const size_t pitch = (size_t)p.Rp * (D + 2);
+  const float* rec = p.part + ((size_t)b0 + (size_t)kvh * nsp) * pitch;
+  float M = -INFINITY;
+  for (int s = lane; s < nsp; s += 32) M = fmaxf(M, __ldcg(rec + s * pitch + row));
+  M = warp_max(M);
+  float lsum = 0.f;
+  float acc[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] = 0.f;
+  for (int s0 = 0; s0 < nsp; s0 += 32) {
+    float w = 0.f, l = 0.f;
+    if (s0 + lane < nsp) {
+      const float ms = __ldcg(rec + (s0 + lane) * pitch + row);
+      l = __ldcg(rec + (s0 + lane) * pitch + p.Rp + row);
+      w = ms == -INFINITY ? 0.f : exp2f(ms - M);
+    }
+    lsum = fmaf(w, l, lsum);
+    const int cnt = min(32, nsp - s0);
+    const float* o = rec + s0 * pitch + 2 * p.Rp + (size_t)row * D + lane * V;
+    int u = 0;
+    for (; u + 4 <= cnt; u += 4) {
+      float x[4][V];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) ld_vec<V>(o + (u + q) * pitch, x[q]);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float wq = __shfl_sync(kFull, w, u + q);
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = fmaf(wq, x[q][i], acc[i]);
+      }
+    }
+    for (; u < cnt; ++u) {
+      float x[V];
+      ld_vec<V>(o + u * pitch, x);
+      const float wq = __shfl_sync(kFull, w, u);
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] = fmaf(wq, x[i], acc[i]);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) lsum += __shfl_xor_sync(kFull, lsum, o);
+  const int t = row / p.G, gq = row - t * p.G;
+  const size_t orow = ((size_t)r * p.T + t) * p.Hq + kvh * p.G + gq;
+  __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(p.out + orow * D + lane * V);
+#pragma unroll
+  for (int i = 0; i < V; i += 2) dst[i / 2] = __floats2bfloat162_rn(acc[i] / lsum, acc[i + 1] / lsum);
+  if (lane == 0) p.lse[orow] = (M + log2f(lsum)) * kLn2;
+}
+
+}  // namespace kv8
+
+static int verify_kv8_npad(int R) { return R <= 16 ? 16 : (R <= 32 ? 32 : (R <= 48 ? 48 : 64)); }
+
+template <int NP, int D>
+static int launch_kv8_t(const CUtensorMap& k1, const CUtensorMap& v1, const CUtensorMap& k8,
+                        const CUtensorMap& v8, const VerifyKv8Params& p, int batch, int num_sms,
+                        cudaStream_t stream) {
+  using C = kv8::Cfg<NP>;
+  static std::atomic<uint64_t> attr_done{0};
+  if (cuda_status(ensure_smem_attr(kv8::verify_kv8_kernel<NP, D>, C::kSmem, attr_done), "cudaFuncSetAttribute") != S3R_OK)
+    return S3R_ERR_CUDA;
+  launch_pdl(kv8::verify_kv8_kernel<NP, D>, num_sms, kv8::kThreads, C::kSmem, stream, k1, v1, k8, v8, p, batch);
+  return cuda_status(cudaGetLastError(), "s3r_verify_attn_kv8");
+}
+
+template <int D>
+static int launch_kv8_d(const CUtensorMap& k1, const CUtensorMap& v1, const CUtensorMap& k8,
+                        const CUtensorMap& v8, const VerifyKv8Params& p, int batch, int num_sms,
+                        cudaStream_t stream) {
+  int st;
+  switch (verify_kv8_npad(p.R)) {
+    case 16: st = launch_kv8_t<16, D>(k1, v1, k8, v8, p, batch, num_sms, stream); break;
+    case 32: st = launch_kv8_t<32, D>(k1, v1, k8, v8, p, batch, num_sms, stream); break;
+    case 48: st = launch_kv8_t<48, D>(k1, v1, k8, v8, p, batch, num_sms, stream); break;
+    default: st = launch_kv8_t<64, D>(k1, v1, k8, v8, p, batch, num_sms, stream); break;
+  }
+  if (st != S3R_OK) return st;
+  dim3 grid((p.R + kv8::kMergeWarps - 1) / kv8::kMergeWarps, p.Hkv, batch);
+  launch_pdl(kv8::merge_kv8_kernel<D>, grid, 32 * kv8::kMergeWarps, 0, stream, p, batch);
+  return cuda_status(cudaGetLastError(), "s3r_verify_attn_kv8 merge");
+}
+
+int launch_verify_kv8(const CUtensorMap& k1, const CUtensorMap& v1, const CUtensorMap& k8,
+                      const CUtensorMap& v8, const VerifyKv8Params& p, int D, int batch, int num_sms,
+                      cudaStream_t stream, int* launches) {
+  *launches = 0;
+  for (int b0 = 0; b0 < batch; b0 += kv8::kMaxBatch) {
+    VerifyKv8Params q = p;
+    q.req_off = b0;
+    const int nb = batch - b0 < kv8::kMaxBatch ? batch - b0 : kv8::kMaxBatch;
+    const int st = D == 128 ? launch_kv8_d<128>(k1, v1, k8, v8, q, nb, num_sms, stream)
+                            : launch_kv8_d<64>(k1, v1, k8, v8, q, nb, num_sms, stream);
+    if (st != S3R_OK) return st;
+    *launches += 2;
+  }
+  return S3R_OK;
+}
+
+// Plan area and span records of one launch (at most kMaxBatch requests): the span length is
+// at least total tiles / (6 spans per SM) (or covers a chunk), so there are at most 6 spans per
+// SM and one more for each (request, KV head).
+size_t verify_kv8_bytes(int num_requests, int Hkv, int R, int D, int num_sms) {
+  const int nb = num_requests < kv8::kMaxBatch ? num_requests : kv8::kMaxBatch;
+  const size_t spans = (size_t)nb * Hkv + (size_t)kSpansPerCta * num_sms;
+  return kv8::kPlanInts * 4 + align_up(spans * (size_t)verify_kv8_rec_rows(R) * (D + 2) * 4, 256);
+}
+
+int verify_kv8_rec_rows(int R) { return (R + 3) / 4 * 4; }
+int verify_kv8_plan_bytes() { return kv8::kPlanInts * 4; }
+
+}  // namespace s3r
