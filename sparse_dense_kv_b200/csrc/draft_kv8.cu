@@ -16,7 +16,9 @@
 //     2t+8, 2t+9, pairs the codes of two positions with byte permutes and converts the pairs.
 // e4m3 -> f16 is exact; q goes to f16 scaled by a power of two per row (a bf16 has 8 significant
 // bits, a half 11: exact down to 2^-21 of the row's largest element, 2^-31 of it off below); P
-// to f16 as 1024 p vs / vsmax (within 2^-11), ks multiplies the logits in fp32.
+// to f16 as 2^(z - mz + 10), z = x + log2 vs and mz its running maximum (within 2^-11, whatever
+// the page scales are), the row sums from 2^(x - m) with the running maximum m of x, in fp32; ks
+// multiplies the logits in fp32.
 //
 // Work: grid (KV head, request, chunk of A_i), 4 warps; warp w takes the chunk's batches of 32
 // positions w, w + 4, .. and runs by itself (lane l resolves position l: index -> page -> row,
@@ -35,6 +37,7 @@ namespace s3r {
 constexpr int kDraftKv8Min = 128;    // one batch of 32 positions per warp
 constexpr int kDraftKv8Max = 1024;
 constexpr int kDraftKv8PerSm = 3;    // resident CTAs
+constexpr float kNoMax = -1e30f;     // a running maximum before its first value
 
 // D = A (16x16 f16, row) * B (16x8 f16, col) + D, fp32 accumulation.
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -146,7 +149,8 @@ __global__ void __launch_bounds__(128, kDraftKv8PerSm) draft_kv8_kernel(const Dr
   for (int j = 0; j < MT; ++j)
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[j][i] = 0.f;
-  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f, vref = 0.f;
+  // running maxima of x and of z, sums relative to the former, O to the latter (- 10)
+  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f, z0 = kNoMax, z1 = kNoMax;
 
   for (int b = start + warp * 32; b < end; b += 128) {
     // row base (in 16 d-byte page blocks) of this lane's position; bad ones read nothing: zeros
@@ -187,7 +191,7 @@ __global__ void __launch_bounds__(128, kDraftKv8PerSm) draft_kv8_kernel(const Dr
     sidx = a < n ? __ldg(sel + a) : -1;
     resolve(a, sidx, page, slot);
     ks = good_scale(ks, p.err);
-    vs = good_scale(vs, p.err);
+    const float lv = log2f(good_scale(vs, p.err));   // -inf: nothing of this position in O
 
     float s[2][4];
 #pragma unroll
@@ -205,32 +209,34 @@ __global__ void __launch_bounds__(128, kDraftKv8PerSm) draft_kv8_kernel(const Dr
       }
     }
     // logits in log2 units; positions g, g + 8 (s[0]), g + 16, g + 24 (s[1]), rows 2t, 2t + 1
-    float mx0 = -INFINITY, mx1 = -INFINITY;
+    float mx0 = -INFINITY, mx1 = -INFINITY, mz0 = z0, mz1 = z1, lvp[2][2];
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int pp = 16 * u + 8 * i + g;
         const float kf = __shfl_sync(kFull, ks, pp);
+        lvp[u][i] = __shfl_sync(kFull, lv, pp);
         const bool in = pp < left;
         s[u][2 * i] = in ? s[u][2 * i] * kf * rf0 : -INFINITY;
         s[u][2 * i + 1] = in ? s[u][2 * i + 1] * kf * rf1 : -INFINITY;
         mx0 = fmaxf(mx0, s[u][2 * i]);
         mx1 = fmaxf(mx1, s[u][2 * i + 1]);
+        mz0 = fmaxf(mz0, s[u][2 * i] + lvp[u][i]);
+        mz1 = fmaxf(mz1, s[u][2 * i + 1] + lvp[u][i]);
       }
 #pragma unroll
     for (int x = 4; x < 32; x <<= 1) {
       mx0 = fmaxf(mx0, __shfl_xor_sync(kFull, mx0, x));
       mx1 = fmaxf(mx1, __shfl_xor_sync(kFull, mx1, x));
+      mz0 = fmaxf(mz0, __shfl_xor_sync(kFull, mz0, x));
+      mz1 = fmaxf(mz1, __shfl_xor_sync(kFull, mz1, x));
     }
-    const float vnew = fmaxf(vref, warp_max(vs));
     const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
-    // -inf only before any position counted (or in a NaN row): nothing to rescale then
-    const float vr_f = vnew > 0.f ? vref / vnew : 0.f;
-    const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - n0), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - n1);
-    l0 *= f0;
-    l1 *= f1;
-    const float o0 = f0 * vr_f, o1 = f1 * vr_f;
+    // m is -inf only before any position counted (or in a NaN row): nothing to rescale then
+    l0 *= m0 == -INFINITY ? 0.f : ex2(m0 - n0);
+    l1 *= m1 == -INFINITY ? 0.f : ex2(m1 - n1);
+    const float o0 = ex2(z0 - mz0), o1 = ex2(z1 - mz1);
 #pragma unroll
     for (int j = 0; j < MT; ++j) {
       o[j][0] *= o0;
@@ -240,20 +246,18 @@ __global__ void __launch_bounds__(128, kDraftKv8PerSm) draft_kv8_kernel(const Dr
     }
     m0 = n0;
     m1 = n1;
-    vref = vnew;
-    const float vn = vnew > 0.f ? 1024.f / vnew : 0.f;
+    z0 = mz0;
+    z1 = mz1;
     uint32_t pf[2][2];   // P^T fragments
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int pp = 16 * u + 8 * i + g;
-        const float w = __shfl_sync(kFull, vs, pp) * vn;
-        // masked places give 2^-inf = 0; a row whose maximum is -inf holds NaN (2^(NaN))
-        const float e0 = ex2(s[u][2 * i] - m0), e1 = ex2(s[u][2 * i + 1] - m1);
-        l0 += e0;
-        l1 += e1;
-        pf[u][i] = movm_t(pack_h2(e0 * w, e1 * w));
+        // masked places give 2^-inf = 0; a row whose maximum is -inf holds NaN (2^NaN)
+        const float x0 = s[u][2 * i], x1 = s[u][2 * i + 1];
+        l0 += ex2(x0 - m0);
+        l1 += ex2(x1 - m1);
+        pf[u][i] = movm_t(pack_h2(ex2(x0 + lvp[u][i] - z0 + 10.f), ex2(x1 + lvp[u][i] - z1 + 10.f)));
       }
 #pragma unroll
     for (int u = 0; u < 2; ++u)
@@ -275,13 +279,15 @@ __global__ void __launch_bounds__(128, kDraftKv8PerSm) draft_kv8_kernel(const Dr
     l0 += __shfl_xor_sync(kFull, l0, x);
     l1 += __shfl_xor_sync(kFull, l1, x);
   }
-  const float vf = vref * (1.f / 1024.f);
+  // O relative to the row maximum: 2^(mz - m - 10) (0 in a warp without positions)
+  const float v0 = m0 == -INFINITY && l0 == 0.f ? 0.f : ex2(z0 - m0 - 10.f);
+  const float v1 = m1 == -INFINITY && l1 == 0.f ? 0.f : ex2(z1 - m1 - 10.f);
   float* ro = redO + (size_t)warp * RW * (D + 4);
 #pragma unroll
   for (int j = 0; j < MT; ++j) {
     const int d0 = g * (D / 8) + 2 * j;
-    *reinterpret_cast<float2*>(ro + (2 * t) * (D + 4) + d0) = make_float2(o[j][0] * vf, o[j][2] * vf);
-    *reinterpret_cast<float2*>(ro + (2 * t + 1) * (D + 4) + d0) = make_float2(o[j][1] * vf, o[j][3] * vf);
+    *reinterpret_cast<float2*>(ro + (2 * t) * (D + 4) + d0) = make_float2(o[j][0] * v0, o[j][2] * v0);
+    *reinterpret_cast<float2*>(ro + (2 * t + 1) * (D + 4) + d0) = make_float2(o[j][1] * v1, o[j][3] * v1);
   }
   if (g == 0) {
     redM[warp * RW + 2 * t] = m0;

@@ -36,21 +36,39 @@ __device__ __forceinline__ float2 unpack_e4m3(uint32_t c2) {
   const uint32_t h = e4m3_to_h2((uint16_t)c2);
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
-// Four values in [0, 256] -> codes h (four) of e4m3(v) and l of e4m3(16 (v - h)). The halves in
+// A pair of values in [0, 256] -> codes h (two) of e4m3(v) and l of e4m3(16 (v - h)). The halves in
 // between hold 11 bits, so h + l / 16 is within 2^-9 of v (plus 2^-14 under the normal range).
-__device__ __forceinline__ void split_e4m3x4(const float (&v)[4], uint32_t& h, uint32_t& l) {
-  uint32_t hc[2], lc[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t x = pack_h2(v[2 * i], v[2 * i + 1]);
-    hc[i] = pack_e4m3_h2(x);
-    const uint32_t back = e4m3_to_h2((uint16_t)hc[i]);
-    const __half2 d = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&back)),
-                              __half2half2(__ushort_as_half((unsigned short)0x4C00)));   // 16
-    lc[i] = pack_e4m3_h2(*reinterpret_cast<const uint32_t*>(&d));
-  }
-  h = hc[0] | (hc[1] << 16);
-  l = lc[0] | (lc[1] << 16);
+__device__ __forceinline__ void split_e4m3x2(float2 v, uint32_t& h, uint32_t& l) {
+  const uint32_t x = pack_h2(v.x, v.y);
+  h = pack_e4m3_h2(x);
+  const uint32_t back = e4m3_to_h2((uint16_t)h);
+  const __half2 d = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&back)),
+                            __half2half2(__ushort_as_half((unsigned short)0x4C00)));   // 16
+  l = pack_e4m3_h2(*reinterpret_cast<const uint32_t*>(&d));
+}
+
+// Packed fp32 pairs (two roundings, one instruction).
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("add.rn.f32x2 %0, %1, %2;\n"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)),
+        "l"(reinterpret_cast<const uint64_t&>(c)));
+  return r;
 }
 
 // A page scale as read: finite and >= 0, else reported and taken as 0.

@@ -15,13 +15,16 @@
 //     scaled to [128, 256): a bf16 value has 8 significant bits and each part holds 4, so the
 //     split is exact down to 2^-10 of the row's largest element and off by at most 2^-18 of it
 //     below. Both parts accumulate into the same S (8 MMAs of K = 32 per tile at d = 128).
-//   p = 256 2^(x - max) vs / vsmax: ph = e4m3(p), pl = e4m3(16 (p - ph)): within 2^-9 of p
-//     (bf16's half step is 2^-9 of the next power of two) and 2^-14 / 256 of the largest weight
-//     below the normal range. The two parts stand side by side along N (2 NP columns), so a tile
-//     takes 4 MMAs; an MMA of M = 128, K = 32 takes about 70 cycles at N = 32 and at N = 64
-//     alike (measured), so the wider product costs no more.
+//   p = 2^(x - m) vs / vsmax, the row's reference m (log2 units) such that its largest p of the
+//     chunk is 256: m = max(x + log2(vs / vsmax)) - 8, so a weight keeps its precision next to
+//     what it contributes to the output, however far the page scales are apart. ph = e4m3(p),
+//     pl = e4m3(16 (p - ph)): within 2^-9 of p (bf16's half step is 2^-9 of the next power of
+//     two), and within 2^-22 of the largest p below the normal range. The two parts stand side by
+//     side along N (2 NP columns), so a tile takes 4 MMAs; an MMA of M = 128, K = 32 takes about
+//     70 cycles at N = 32 and at N = 64 alike (measured), so the wider product costs no more.
 // The scales enter in fp32: ks times the logit of its position (one tensor-memory lane = one
-// position = one page), vs into p, relative to the chunk's largest.
+// position = one page), vs / vsmax of the chunk into p, vsmax into the chunk's O. The row sums are
+// those of 2^(x - m) in fp32; m need not be the row's maximum (it is at least that - 72).
 //
 // Organisation: one persistent CTA per SM. A work item is a span of consecutive tiles of 128
 // positions of one (request, KV head); spans are claimed from a counter in the workspace. A span
@@ -56,6 +59,8 @@ constexpr int kSoftWarp0 = 4;
 constexpr int kTileBytes = kPos * 128;    // 16 KB: 128 positions x 128 bytes (d = 64: half zero)
 constexpr int kRing = 16;
 constexpr int kScaleBufs = 4;             // chunks whose page scales are held
+constexpr int kScaleFloats = 196;         // ks, vs / vsmax, log2 of that (>= -64) [64] each; vsmax; pad
+constexpr int kBarBytes = 1792;           // barriers, flags, the ring of spans
 constexpr int kMaxBatch = 256;            // requests per launch (larger batches: several launches)
 // plan area of the workspace (written by the attention kernel for the merge): span length in
 // tiles, then the prefix of per-request span counts
@@ -101,16 +106,22 @@ struct Cfg {
   static constexpr int kQOff = kVOff + kVSt * kTileBytes;
   static constexpr int kPOff = kQOff + 2 * kQBytes;
   static constexpr int kRedOff = kPOff + kPT * kPTile;
-  // floats: redM, redL [8 warps][NH]; cm, fa, fb, rm, rl [2][NP]; rs [4][NP]; scales [4][2][64]
-  static constexpr int kRedFloats = 2 * 8 * (NP / 2) + 5 * 2 * NP + 4 * NP + kScaleBufs * 128;
+  // floats: redM, redL [2][8 warps][NH]; per-warp rows [8][5][NH]; rs [4][NP]; scales [4][196]
+  static constexpr int kRedFloats = 2 * 2 * 8 * (NP / 2) + 8 * 5 * (NP / 2) + 4 * NP + kScaleBufs * kScaleFloats;
   static constexpr int kPrefOff = kRedOff + kRedFloats * 4;
   static constexpr int kLenOff = kPrefOff + (kMaxBatch + 4) * 4;
   static constexpr int kRidOff = kLenOff + kMaxBatch * 4;
   static constexpr int kIdsOff = kRidOff + kMaxBatch * 4;
   static constexpr int kBarOff = (kIdsOff + 2 * 64 * 4 + 63) / 64 * 64;
-  static constexpr int kSmem = kBarOff + 1280 + 1024;
+  static constexpr int kSmem = kBarOff + kBarBytes + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
   static_assert(kQOff % 1024 == 0 && kPOff % 1024 == 0 && kRedOff % 16 == 0, "operand alignment");
+};
+
+// A span of tiles [t0, t1) of (request r, KV head kvh), one of nsp; L committed positions.
+// id < 0: the launch has no more work.
+struct Span {
+  int id, r, kvh, nsp, L, t0, t1, pad;
 };
 
 struct Bars {
@@ -125,17 +136,12 @@ struct Bars {
   uint64_t fin[2];
   uint64_t wg[2];
   uint64_t item_bar[kRing];
-  int item_id[kRing];
+  int4 span[kRing][2];                   // the CTA's m-th span at m % kRing
   uint32_t tmem_base;
   int abort_flag;
-  int span;                              // tiles per span of this launch
+  int span_tiles;                        // tiles per span of this launch
 };
-static_assert(sizeof(Bars) <= 1280, "barrier block");
-
-// A span of tiles [t0, t1) of (request r, KV head kvh); L committed positions, Lc = L + T.
-struct Span {
-  int id, r, kvh, s, nsp, L, Lc, t0, t1;
-};
+static_assert(sizeof(Bars) <= kBarBytes && sizeof(Span) == 32, "barrier block");
 
 __device__ __forceinline__ Span make_span(int id, const int* pref, const int* lens_s, const int* rid_s,
                                           int batch, int Hkv, int T, int st) {
@@ -150,12 +156,11 @@ __device__ __forceinline__ Span make_span(int id, const int* pref, const int* le
   const int rem = id - pref[lo];
   x.nsp = (pref[lo + 1] - pref[lo]) / Hkv;
   x.kvh = rem / x.nsp;
-  x.s = rem - x.kvh * x.nsp;
   x.r = rid_s[lo];
   x.L = lens_s[lo];
-  x.Lc = x.L + T;
-  x.t0 = x.s * st;
-  x.t1 = min(x.t0 + st, (x.Lc + kPos - 1) / kPos);
+  x.t0 = (rem - x.kvh * x.nsp) * st;
+  x.t1 = min(x.t0 + st, (x.L + T + kPos - 1) / kPos);
+  x.pad = 0;
   return x;
 }
 
@@ -195,6 +200,18 @@ struct ColReduce {
   }
 };
 
+// Values of a tensor-memory load may be used from here on: ties the registers behind the wait.
+template <int N>
+__device__ __forceinline__ void tmem_tie(float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
+}
+template <int N>
+__device__ __forceinline__ void tmem_ready(float (&v)[N]) {
+  tmem_wait_ld();
+  tmem_tie(v);
+}
+
 template <int NP, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     verify_kv8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -205,15 +222,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int NH = NP / 2;
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
-  float* redM = reinterpret_cast<float*>(smem + C::kRedOff);   // [8][NH]
-  float* redL = redM + 8 * NH;                                  // [8][NH]
-  float* cm = redL + 8 * NH;                                    // [2][NP] chunk max (log2 units)
-  float* fa = cm + 2 * NP;                                      // [2][NP] factor of the running O
-  float* fb = fa + 2 * NP;                                      // [2][NP] factor of the chunk's O
-  float* rm = fb + 2 * NP;                                      // [2][NP] running max
-  float* rl = rm + 2 * NP;                                      // [2][NP] running sum
-  float* rs = rl + 2 * NP;                                      // [4][NP] q row factor 2^e / sqrt(d)
-  float* scs = rs + 4 * NP;                                     // [4][2][64] page scales (ks, vs)
+  float* redM = reinterpret_cast<float*>(smem + C::kRedOff);   // [2][8][NH] warp maxima (chunk parity)
+  float* redL = redM + 2 * 8 * NH;                              // [2][8][NH] warp sums
+  float* own = redL + 2 * 8 * NH;                               // [8][5][NH] per warp: max, a, b, run max, run sum
+  float* rs = own + 8 * 5 * NH;                                 // [4][NP] q row factor 2^e / sqrt(d)
+  float* scs = rs + 4 * NP;                                     // [4][196] page scales
   int* pref = reinterpret_cast<int*>(smem + C::kPrefOff);
   int* lens_s = reinterpret_cast<int*>(smem + C::kLenOff);
   int* rid_s = reinterpret_cast<int*>(smem + C::kRidOff);
@@ -299,25 +312,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (lane == 0) {
       pref[0] = 0;
-      B->span = st;
+      B->span_tiles = st;
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = B->tmem_base;
-  const int nitems = pref[batch], st = B->span;
+  const int nitems = pref[batch], st = B->span_tiles;
   if (blockIdx.x == 0)   // the merge's plan
     for (int b = tid; b <= batch + 1; b += blockDim.x) p.plan[b] = b == 0 ? st : pref[b - 1];
 
   // A CTA's first span is blockIdx.x, later ones come from the launch's counter; the K producer
-  // claims them and publishes the ids in a ring (id >= nitems: no more work).
-  auto ring_id = [&](int m) -> int {   // warp-uniform; -1 if the wait gave up
+  // claims them and publishes them in a ring (id < 0: no more work).
+  auto ring_span = [&](int m, Span& x) -> bool {   // false: no more work, or the wait gave up
     const int slot = m & (kRing - 1);
-    if (!wait_bar(smem_u32(&B->item_bar[slot]), (uint32_t)(m / kRing) & 1u, abort_flag, p.err, p.wait_limit)) return -1;
-    return *reinterpret_cast<volatile int*>(&B->item_id[slot]);
+    if (!wait_bar(smem_u32(&B->item_bar[slot]), (uint32_t)(m / kRing) & 1u, abort_flag, p.err, p.wait_limit)) return false;
+    const int4 a = B->span[slot][0], b = B->span[slot][1];
+    x.id = a.x; x.r = a.y; x.kvh = a.z; x.nsp = a.w;
+    x.L = b.x; x.t0 = b.y; x.t1 = b.z;
+    return x.id >= 0;
   };
-  auto span_of = [&](int id) { return make_span(id, pref, lens_s, rid_s, batch, Hkv, T, st); };
   auto waitb = [&](uint64_t* bar, int phase) -> bool {
     return wait_bar(smem_u32(bar), (uint32_t)phase & 1u, abort_flag, p.err, p.wait_limit);
   };
@@ -344,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Page ids of the chunk [t0, t1), two per lane (-1 past the context or outside the pool).
     auto fetch_ids = [&](const Span& x, int t0, int t1, int& a, int& b) {
       const int* ptab = p.page_table + (size_t)x.r * p.max_pages;
-      const int npg = (t1 - t0) * 8, pg0 = t0 * 8, pend = (x.Lc + kPage - 1) / kPage;
+      const int npg = (t1 - t0) * 8, pg0 = t0 * 8, pend = (x.L + T + kPage - 1) / kPage;
       a = lane < npg && pg0 + lane < pend ? ptab[pg0 + lane] : -1;
       b = lane + 32 < npg && pg0 + lane + 32 < pend ? ptab[pg0 + lane + 32] : -1;
     };
@@ -355,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
       }
       const uint32_t dst = sbase + roff + s * kTileBytes;
-      const int pend = (x.Lc + kPage - 1) / kPage;
+      const int Lc = x.L + T, pend = (Lc + kPage - 1) / kPage;
       // one page per lane (lanes 0..7)
       const int pg = t * 8 + lane;
       const int id = lane < 8 ? ids_own[i0 + lane] : -1;
@@ -367,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int id0 = __shfl_sync(kFull, id, 0);
       const bool run = __all_sync(kFull, lane >= 8 || (good && id == id0 + lane));
       // rows that must read as zero: a bad page's, and for V every row behind the context
-      const bool patch = okmask != wantmask || (is_v && (t + 1) * kPos > x.Lc);
+      const bool patch = okmask != wantmask || (is_v && (t + 1) * kPos > Lc);
       const uint32_t landing = smem_u32(patch ? &tmab[s] : &full[s]);
       if (lane == 0) mbar_arrive_expect_tx(landing, (uint32_t)__popc(okmask) * kPage * 128);
       __syncwarp();
@@ -387,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_phase ^= 1u << s;
         for (int idx = lane; idx < kPos * 8; idx += 32) {
           const int row = idx >> 3;
-          if ((okmask & (1u << (row >> 4))) && !(is_v && t * kPos + row >= x.Lc)) continue;
+          if ((okmask & (1u << (row >> 4))) && !(is_v && t * kPos + row >= Lc)) continue;
           *reinterpret_cast<uint4*>(smem + roff + s * kTileBytes + idx * 16) = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async();
@@ -396,21 +411,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     };
-    auto item_id = [&](int m) -> int {
-      if (is_v) return ring_id(m);
+    // the CTA's m-th span: claimed and published by the K producer, read by the V producer
+    auto next_span = [&](int m, Span& x) -> bool {
+      if (is_v) return ring_span(m, x);
       int id = (int)blockIdx.x;
       if (m > 0) {
         int v = 0;
         if (lane == 0) v = atomicAdd(p.sched, 1);
         id = __shfl_sync(kFull, v, 0) + (int)gridDim.x;
       }
-      id = min(id, nitems);
+      if (id < nitems) x = make_span(id, pref, lens_s, rid_s, batch, Hkv, T, st);
+      else x.id = -1;
       if (lane == 0) {
-        B->item_id[m & (kRing - 1)] = id;
-        mbar_arrive(smem_u32(&B->item_bar[m & (kRing - 1)]));   // release: the id is visible
+        const int slot = m & (kRing - 1);
+        B->span[slot][0] = make_int4(x.id, x.r, x.kvh, x.nsp);
+        B->span[slot][1] = make_int4(x.L, x.t0, x.t1, 0);
+        mbar_arrive(smem_u32(&B->item_bar[slot]));   // release: the span is visible
       }
       __syncwarp();
-      return id;
+      return x.id >= 0;
     };
     // q rows of span m -> buffer m & 1 (V producer), once the QK of span m - 2 has read it
     constexpr int LR = D / 8;          // lanes per row (8 elements each)
@@ -478,11 +497,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // The chunk after (x, t0): the next of the span, or the first of the next span.
     int m = 0, n = 0;   // span and chunk counters
-    int cur = item_id(0);
     Span x{};
     int t0 = 0, t1 = 0, ida = -1, idb = -1;
-    if (cur >= 0 && cur < nitems) {
-      x = span_of(cur);
+    bool more = next_span(0, x);
+    if (more) {
       t0 = x.t0;
       t1 = min(t0 + C::kMT, x.t1);
       fetch_ids(x, t0, t1, ida, idb);
@@ -491,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!split_q(x, 0)) stop = true;
       }
     }
-    while (cur >= 0 && cur < nitems && !stop && !aborted(abort_flag)) {
+    while (more && !stop && !aborted(abort_flag)) {
       __syncwarp();
       ids_own[lane] = ida;
       ids_own[lane + 32] = idb;
@@ -514,32 +532,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       load_tile(x, t0, 0);
       if (stop) break;
       if (!is_v) {
-        float* sc = scs + (n & (kScaleBufs - 1)) * 128;
+        float* sc = scs + (n & (kScaleBufs - 1)) * kScaleFloats;
+        va = good_scale(va, p.err);
+        vb = good_scale(vb, p.err);
+        const float vmax = warp_max(fmaxf(va, vb));
+        const float vnorm = vmax >= 0x1p-120f ? 1.f / vmax : 0.f;   // smaller scales count as zero
         sc[lane] = good_scale(ka, p.err);
         sc[lane + 32] = good_scale(kb, p.err);
-        sc[64 + lane] = good_scale(va, p.err);
-        sc[64 + lane + 32] = good_scale(vb, p.err);
+        sc[64 + lane] = va * vnorm;
+        sc[64 + lane + 32] = vb * vnorm;
+        sc[128 + lane] = fmaxf(log2f(va * vnorm), -64.f);
+        sc[128 + lane + 32] = fmaxf(log2f(vb * vnorm), -64.f);
+        if (lane == 0) sc[192] = vmax;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&B->sc_full[n & (kScaleBufs - 1)]));
       }
       // what comes next is claimed and its page ids are fetched while this chunk streams
-      int nt0 = t1, nt1, na, nb, nxt = cur;
+      int nt0 = t1, na = -1, nb = -1;
       Span xn = x;
       if (t1 >= x.t1) {
-        nxt = item_id(++m);
-        if (nxt >= 0 && nxt < nitems) {
-          xn = span_of(nxt);
-          nt0 = xn.t0;
-        }
+        more = next_span(++m, xn);
+        nt0 = xn.t0;
       }
-      nt1 = min(nt0 + C::kMT, xn.t1);
-      na = nb = -1;
-      if (nxt >= 0 && nxt < nitems) {
+      const int nt1 = min(nt0 + C::kMT, xn.t1);
+      if (more) {
         fetch_ids(xn, nt0, nt1, na, nb);
         if (is_v && t1 >= x.t1 && !split_q(xn, m)) stop = true;
       }
       for (int t = t0 + 1; t < t1 && !stop; ++t) load_tile(x, t, (t - t0) * 8);
-      cur = nxt;
       x = xn;
       t0 = nt0;
       t1 = nt1;
@@ -555,9 +575,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int gk = 0, n = 0;
     bool ok = true;
     for (int m = 0; ok; ++m) {
-      const int id = ring_id(m);
-      if (id < 0 || id >= nitems) break;
-      const Span x = span_of(id);
+      Span x;
+      if (!ring_span(m, x)) break;
       if (!waitb(&B->q_full[m & 1], m >> 1)) break;
       for (int t0 = x.t0; t0 < x.t1 && ok; t0 += C::kMT, ++n) {
         // at most two chunks ahead of the softmax (per-chunk buffers)
@@ -603,9 +622,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int gv = 0, n = 0;
     bool ok = true;
     for (int m = 0; ok; ++m) {
-      const int id = ring_id(m);
-      if (id < 0 || id >= nitems) break;
-      const Span x = span_of(id);
+      Span x;
+      if (!ring_span(m, x)) break;
       for (int t0 = x.t0; t0 < x.t1 && ok; t0 += C::kMT, ++n) {
         if (n >= 2 && !waitb(&B->o_empty[n & 1], (n - 2) >> 1)) {
           ok = false;
@@ -645,7 +663,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ================================================================ softmax warps ====
     const int sg = (warp - kSoftWarp0) >> 2;        // warpgroup: rows [sg NH, sg NH + NH)
     const int q4 = warp & 3;                        // tensor-memory lane quarter
-    const int gt = (tid - 32 * kSoftWarp0) & 127;   // thread within the warpgroup
     const int lrow = q4 * 32 + lane;                // tile position (S) or d (O) of this thread
     const int c0 = sg * NH;
     const bool lead8 = (c0 & 15) == 8;
@@ -660,28 +677,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       wg_phase ^= 1u;
       return r;
     };
+    constexpr bool kHeld = NH <= 16;   // row constants in registers (24 and 32 rows spill)
+    float* cmw = own + (sg * 4 + q4) * 5 * NH;   // this warp's copies of the group's rows: reference,
+    float* faw = cmw + NH;                       //   factor of the running O, of the chunk's O,
+    float* fbw = faw + NH;                       //   running max and running sum
+    float* rmw = fbw + NH;
+    float* rlw = rmw + NH;
     float orun[NH];   // running O of the span (this thread's d), relative to the running max
     // Chunk n's O joins the span; with its last chunk the span's record (or, when the span is the
     // whole context, the output) is written.
     auto epilogue = [&](int n, const Span& x, bool first, bool last) -> bool {
       if (!waitb(&B->o_full[n & 1], n >> 1)) return false;
       tc_fence_after();
-      const float* fan = fa + (n & 1) * NP + c0;
-      const float* fbn = fb + (n & 1) * NP + c0;
       float o[NP];
       tmem_ld<NP>(tl + (n & 1) * C::kOCols + sg * NP, o);
-      tmem_wait_ld();
-#pragma unroll
-      for (int j = 0; j < NH; ++j) {
-        const float v = fmaf(o[NH + j], 0.0625f, o[j]) * fbn[j];
-        orun[j] = first ? v : fmaf(orun[j], fan[j], v);
-      }
+      tmem_ready(o);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&B->o_empty[n & 1]));
+#pragma unroll
+      for (int j = 0; j < NH; j += 4) {
+        const float4 a = *reinterpret_cast<const float4*>(faw + j), b = *reinterpret_cast<const float4*>(fbw + j);
+        const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float v = fmaf(o[NH + j + i], 0.0625f, o[j + i]) * bv[i];
+          orun[j + i] = first ? v : fmaf(orun[j + i], av[i], v);
+        }
+      }
       if (!last) return true;
-      const float* rmn = rm + (n & 1) * NP + c0;
-      const float* rln = rl + (n & 1) * NP + c0;
       if (x.nsp == 1) {
         if (lrow < D) {
 #pragma unroll
@@ -689,13 +713,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int row = c0 + j;
             if (row < R) {
               const int t = row / G, gq = row - t * G;
-              p.out[(((size_t)x.r * T + t) * p.Hq + x.kvh * G + gq) * D + lrow] = __float2bfloat16_rn(orun[j] / rln[j]);
+              p.out[(((size_t)x.r * T + t) * p.Hq + x.kvh * G + gq) * D + lrow] = __float2bfloat16_rn(orun[j] / rlw[j]);
             }
           }
         }
-        if (gt < NH && c0 + gt < R) {
-          const int row = c0 + gt, t = row / G, gq = row - t * G;
-          p.lse[((size_t)x.r * T + t) * p.Hq + x.kvh * G + gq] = (rmn[gt] + log2f(rln[gt])) * kLn2;
+        if (q4 == 0 && lane < NH && c0 + lane < R) {
+          const int row = c0 + lane, t = row / G, gq = row - t * G;
+          p.lse[((size_t)x.r * T + t) * p.Hq + x.kvh * G + gq] = (rmw[lane] + log2f(rlw[lane])) * kLn2;
         }
         return true;
       }
@@ -705,152 +729,220 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < NH; ++j)
           if (c0 + j < R) rec[2 * p.Rp + (size_t)(c0 + j) * D + lrow] = orun[j];
       }
-      if (gt < NH && c0 + gt < R) {
-        rec[c0 + gt] = rmn[gt];
-        rec[p.Rp + c0 + gt] = rln[gt];
+      if (q4 == 0 && lane < NH && c0 + lane < R) {
+        rec[c0 + lane] = rmw[lane];
+        rec[p.Rp + c0 + lane] = rlw[lane];
       }
       return true;
     };
 
     bool ok = true;
     int n = 0, gs = 0;          // chunk and tile counters
-    float mrun = 0.f, lrun = 0.f;   // of row c0 + gt (threads gt < NH)
+    // Lane j of every warp of the group keeps row c0 + j: running max and sum of the span, maximum
+    // and V factor of the last chunk. The four warps hold the same values, so one barrier per chunk
+    // (the maxima of this chunk, the sums of the one before) is all they need.
+    float mrun = 0.f, lrun = 0.f, mcp = 0.f, ovp = 0.f;
+    const int jl = lane < NH ? lane : NH - 1;
     Span xp{};
     bool pfirst = false, plast = false;
+    // chunk n - 1 (its sums complete) joins the running state
+    auto join = [&](int n1) {
+      const float* rl4 = redL + (n1 & 1) * 8 * NH + sg * 4 * NH + jl;
+      const float l = (rl4[0] + rl4[NH]) + (rl4[2 * NH] + rl4[3 * NH]);
+      float a = 0.f, b = ovp;
+      if (pfirst) {
+        mrun = mcp;
+        lrun = l;
+      } else {
+        const float mn = fmaxf(mrun, mcp);
+        a = mrun == -INFINITY ? 0.f : exp2f(mrun - mn);
+        const float bb = mcp == -INFINITY ? 0.f : exp2f(mcp - mn);
+        b = bb * ovp;
+        lrun = lrun * a + l * bb;
+        mrun = mn;
+      }
+      if (lane < NH) {
+        faw[lane] = a;
+        fbw[lane] = b;
+        rmw[lane] = mrun;
+        rlw[lane] = lrun;
+      }
+    };
     for (int m = 0; ok && !aborted(abort_flag); ++m) {
-      const int id = ring_id(m);
-      if (id < 0) ok = false;
-      if (id < 0 || id >= nitems) break;
-      const Span x = span_of(id);
-      const int L = x.L, Lc = x.Lc;
+      Span x;
+      if (!ring_span(m, x)) break;
+      const int L = x.L, Lc = x.L + T;
       float* scores = p.scores ? p.scores + ((size_t)x.r * Hkv + x.kvh) * (size_t)R * p.cap : nullptr;
       const float* rsm = rs + (m & 3) * NP + c0;
       for (int t0 = x.t0; t0 < x.t1 && ok; t0 += C::kMT, ++n) {
         const int t1 = min(t0 + C::kMT, x.t1), nt = t1 - t0;
         const bool first = t0 == x.t0, last = t1 == x.t1;
-        if (!waitb(&B->sc_full[n & (kScaleBufs - 1)], n / kScaleBufs)) {
+        // the chunk's page scales, and with its first tile the span's row factors
+        if (!waitb(&B->sc_full[n & (kScaleBufs - 1)], n / kScaleBufs) ||
+            !waitb(&B->sfull[gs % C::kNS], gs / C::kNS)) {
           ok = false;
           break;
         }
-        const float* ksc = scs + (n & (kScaleBufs - 1)) * 128;
+        const float* ksc = scs + (n & (kScaleBufs - 1)) * kScaleFloats + (lrow >> 4);   // + 8 per tile
         const float* vsc = ksc + 64;
-        const float vmax = warp_max(fmaxf(vsc[lane], vsc[lane + 32]));
-        const float vnorm = vmax > 0.f ? 256.f / vmax : 0.f;   // a scale under 2^-118 counts as zero
+        const float* lvc = ksc + 128;
+        const float vmax = scs[(n & (kScaleBufs - 1)) * kScaleFloats + 192];
 
-        // pass 1: committed logits out, row maxima (of acc * ks: the row factor is positive)
-        float mrow[NH];
+        // pass 1: committed logits out, per row the maximum of x + log2(vs / vsmax); two tiles per
+        // step up to 16 rows
+        float2 mrow[NH / 2], rs2[kHeld ? NH / 2 : 1];   // maxima; row factors (log2 units)
 #pragma unroll
-        for (int j = 0; j < NH; ++j) mrow[j] = -INFINITY;
-        for (int u = 0; u < nt; ++u) {
-          const int d = (gs + u) % C::kNS;
-          if (!waitb(&B->sfull[d], (gs + u) / C::kNS)) {
+        for (int j = 0; j < NH / 2; ++j) {
+          mrow[j] = make_float2(-INFINITY, -INFINITY);
+          if constexpr (kHeld) rs2[j] = make_float2(rsm[2 * j] * kLog2e, rsm[2 * j + 1] * kLog2e);
+        }
+        auto row_factor = [&](int j) -> float2 {   // of rows 2j, 2j + 1
+          if constexpr (kHeld) return rs2[j];
+          else return mul2(*reinterpret_cast<const float2*>(rsm + 2 * j), make_float2(kLog2e, kLog2e));
+        };
+        constexpr int U = kHeld ? 2 : 1;
+        for (int u0 = 0; u0 < nt && ok; u0 += U) {
+          float v[U][NH];
+          const int ul = min(u0 + U, nt) - 1;   // an odd last tile is taken twice
+          if (!waitb(&B->sfull[(gs + ul) % C::kNS], (gs + ul) / C::kNS)) {   // tiles complete in order
             ok = false;
             break;
           }
           tc_fence_after();
-          float v[NH];
-          tmem_ld_cols<NH>(tl + C::kSCol0 + d * NP + c0, v, lead8);
+#pragma unroll
+          for (int w = 0; w < U; ++w)
+            tmem_ld_cols<NH>(tl + C::kSCol0 + (gs + min(u0 + w, ul)) % C::kNS * NP + c0, v[w], lead8);
           tmem_wait_ld();
-          const int p0 = (t0 + u) * kPos, pos = p0 + lrow;
-          const float ks = ksc[u * 8 + (lrow >> 4)];
 #pragma unroll
-          for (int j = 0; j < NH; ++j) v[j] *= ks;
-          if (scores && pos < L) {
-            float* srow = scores + (size_t)c0 * p.cap + pos;
+          for (int w = 0; w < U; ++w) tmem_tie(v[w]);
 #pragma unroll
-            for (int j = 0; j < NH; ++j)
-              if (c0 + j < R) srow[(size_t)j * p.cap] = v[j] * rsm[j];
-          }
-          if (p0 + kPos <= L) {
+          for (int w = 0; w < U; ++w) {
+            const int u = min(u0 + w, ul);
+            const int p0 = (t0 + u) * kPos, pos = p0 + lrow;
+            const float ks = ksc[u * 8];
+            const float2 ks2 = make_float2(ks, ks);
+            float2 y[NH / 2];
 #pragma unroll
-            for (int j = 0; j < NH; ++j) mrow[j] = fmaxf(mrow[j], v[j]);
-          } else {
+            for (int j = 0; j < NH / 2; ++j) y[j] = mul2(make_float2(v[w][2 * j], v[w][2 * j + 1]), ks2);
+            if (scores && pos < L && u == u0 + w) {
+              float* srow = scores + (size_t)c0 * p.cap + pos;
 #pragma unroll
-            for (int j = 0; j < NH; ++j) {
-              const int row = c0 + j;
-              if (pos < Lc && row < R && (pos < L || (pos - L) * G <= row)) mrow[j] = fmaxf(mrow[j], v[j]);
+              for (int j = 0; j < NH / 2; ++j) {
+                if (c0 + 2 * j < R) srow[(size_t)(2 * j) * p.cap] = y[j].x * rsm[2 * j];
+                if (c0 + 2 * j + 1 < R) srow[(size_t)(2 * j + 1) * p.cap] = y[j].y * rsm[2 * j + 1];
+              }
+            }
+            const float lv = lvc[u * 8];
+            const float2 lv2 = make_float2(lv, lv);
+#pragma unroll
+            for (int j = 0; j < NH / 2; ++j) y[j] = fma2(y[j], row_factor(j), lv2);
+            if (p0 + kPos > L) {
+              // row sees the position: pos < Lc and pos - L <= t, the row's block row
+              const int r0 = pos < L ? 0 : (pos < Lc ? (pos - L) * G : kPos);   // first row that sees it
+#pragma unroll
+              for (int j = 0; j < NH / 2; ++j) {
+                if (c0 + 2 * j < r0 || c0 + 2 * j >= R) y[j].x = -INFINITY;
+                if (c0 + 2 * j + 1 < r0 || c0 + 2 * j + 1 >= R) y[j].y = -INFINITY;
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < NH / 2; ++j) {
+              mrow[j].x = fmaxf(mrow[j].x, y[j].x);
+              mrow[j].y = fmaxf(mrow[j].y, y[j].y);
             }
           }
         }
         if (!ok) break;
         {
-          const float r = ColReduce<NH>::run(mrow, lane, -INFINITY, [](float a, float b) { return fmaxf(a, b); });
+          float mx[NH];
+#pragma unroll
+          for (int j = 0; j < NH; ++j) mx[j] = (j & 1) ? mrow[j / 2].y : mrow[j / 2].x;
+          const float r = ColReduce<NH>::run(mx, lane, -INFINITY, [](float a, float b) { return fmaxf(a, b); });
           const int c = ColReduce<NH>::col_of(lane);
-          if (c < NH) redM[(sg * 4 + q4) * NH + c] = r;
+          if (c < NH) redM[((n & 1) * 8 + sg * 4 + q4) * NH + c] = r;
         }
         if (!wg_sync()) {
           ok = false;
           break;
         }
-        float mc = -INFINITY;
-        if (gt < NH) {
-#pragma unroll
-          for (int w = 0; w < 4; ++w) mc = fmaxf(mc, redM[(sg * 4 + w) * NH + gt]);
-          mc *= rsm[gt] * kLog2e;
-          if (c0 + gt >= R) mc = 0.f;
-          cm[(n & 1) * NP + c0 + gt] = mc;
+        if (n > 0) join(n - 1);
+        {
+          const float* m4 = redM + (n & 1) * 8 * NH + sg * 4 * NH + jl;
+          const float mx = fmaxf(fmaxf(m4[0], m4[NH]), fmaxf(m4[2 * NH], m4[3 * NH]));
+          mcp = mx - 8.f;
+          ovp = vmax;
+          if (lane < NH) cmw[lane] = mcp;
         }
-        if (!wg_sync()) {
-          ok = false;
-          break;
-        }
-        // row maxima and factors: registers up to 16 rows, beyond that re-read from shared memory
-        // tile by tile (24 and 32 rows spill otherwise)
-        constexpr bool kHeld = NH <= 16;
-        const float* cmn = cm + (n & 1) * NP + c0;
-        float rs2[kHeld ? NH : 1], lsum[NH];
+        __syncwarp();
+        float2 nm[kHeld ? NH / 2 : 1], lsum[NH / 2];   // -reference, sums
 #pragma unroll
-        for (int j = 0; j < NH; ++j) {
-          if constexpr (kHeld) {
-            mrow[j] = cmn[j];
-            rs2[j] = rsm[j] * kLog2e;
-          }
-          lsum[j] = 0.f;
+        for (int j = 0; j < NH / 2; ++j) {
+          if constexpr (kHeld) nm[j] = make_float2(-cmw[2 * j], -cmw[2 * j + 1]);
+          lsum[j] = make_float2(0.f, 0.f);
         }
 
-        // pass 2: p = 2^(x - max); its sum in fp32, 256 p vs / vsmax in two e4m3 parts to P^T
+        // pass 2: 2^(x - m), its sum in fp32, times vs / vsmax in two e4m3 parts to P^T. The
+        // next tile's logits are on their way while this one is worked on, and a tile's P^T is
+        // handed over once the next one is ready to be stored (its stores have drained by then).
+        float v[NH];
+        tmem_ld_cols<NH>(tl + C::kSCol0 + gs % C::kNS * NP + c0, v, lead8);
+        auto publish = [&](int slot) {
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&B->pfull[slot]));
+        };
         for (int u = 0; u < nt; ++u) {
-          const int d = (gs + u) % C::kNS;
-          float v[NH];
-          tmem_ld_cols<NH>(tl + C::kSCol0 + d * NP + c0, v, lead8);
           tmem_wait_ld();
+          tmem_tie(v);
+          float w[NH];
+#pragma unroll
+          for (int j = 0; j < NH; ++j) w[j] = v[j];
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&B->sempty[d]));
+          if (lane == 0) mbar_arrive(smem_u32(&B->sempty[(gs + u) % C::kNS]));
+          if (u + 1 < nt) tmem_ld_cols<NH>(tl + C::kSCol0 + (gs + u + 1) % C::kNS * NP + c0, v, lead8);
           const int p0 = (t0 + u) * kPos, pos = p0 + lrow;
-          const float ks = ksc[u * 8 + (lrow >> 4)];
-          const float vw = vsc[u * 8 + (lrow >> 4)] * vnorm;
+          const float ks = ksc[u * 8], vw = vsc[u * 8];
+          const float2 ks2 = make_float2(ks, ks), vw2 = make_float2(vw, vw);
           const bool interior = p0 + kPos <= L;
+          const int r0 = interior || pos < L ? 0 : (pos < Lc ? (pos - L) * G : kPos);
           uint32_t hb[NH / 4], lb[NH / 4];
 #pragma unroll
           for (int j = 0; j < NH; j += 4) {
-            float e[4], mj[4], rj[4];
+            float2 e[2], mj[2];
             if constexpr (kHeld) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                mj[i] = mrow[j + i];
-                rj[i] = rs2[j + i];
-              }
+              mj[0] = nm[j / 2];
+              mj[1] = nm[j / 2 + 1];
             } else {
-              const float4 m4 = *reinterpret_cast<const float4*>(cmn + j);
-              const float4 r4 = *reinterpret_cast<const float4*>(rsm + j);
-              mj[0] = m4.x; mj[1] = m4.y; mj[2] = m4.z; mj[3] = m4.w;
-              rj[0] = r4.x * kLog2e; rj[1] = r4.y * kLog2e; rj[2] = r4.z * kLog2e; rj[3] = r4.w * kLog2e;
+              const float4 m4 = *reinterpret_cast<const float4*>(cmw + j);
+              mj[0] = make_float2(-m4.x, -m4.y);
+              mj[1] = make_float2(-m4.z, -m4.w);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              e[i] = ex2(fmaf(v[j + i] * ks, rj[i], -mj[i]));
-              if (!interior) {
-                const int row = c0 + j + i;
-                const bool vis = pos < Lc && row < R && (pos < L || (pos - L) * G <= row) && mj[i] != -INFINITY;
-                e[i] = vis ? e[i] : 0.f;
-              }
-              lsum[j + i] += e[i];
-              e[i] *= vw;
+            for (int i = 0; i < 2; ++i) {
+              e[i] = fma2(mul2(make_float2(w[j + 2 * i], w[j + 2 * i + 1]), ks2), row_factor(j / 2 + i), mj[i]);
+              e[i] = make_float2(ex2(e[i].x), ex2(e[i].y));
             }
-            split_e4m3x4(e, hb[j / 4], lb[j / 4]);
+            if (!interior) {
+              // (a row that sees something of the chunk and still has maximum -inf holds NaN, and keeps it)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int row = c0 + j + 2 * i;
+                if (row < r0 || row >= R) e[i].x = 0.f;
+                if (row + 1 < r0 || row + 1 >= R) e[i].y = 0.f;
+              }
+            }
+            uint32_t h[2], l[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              lsum[j / 2 + i] = add2(lsum[j / 2 + i], e[i]);
+              split_e4m3x2(mul2(e[i], vw2), h[i], l[i]);
+            }
+            hb[j / 4] = __byte_perm(h[0], h[1], 0x5410);
+            lb[j / 4] = __byte_perm(l[0], l[1], 0x5410);
           }
           const int gp = gs + u, slot = gp % C::kPT;
+          if (u > 0) publish((gp - 1) % C::kPT);
           if (gp >= C::kPT && !waitb(&B->pfree[slot], gp / C::kPT - 1)) {
             ok = false;
             break;
@@ -858,27 +950,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           // this warpgroup's NP bytes of the position's row: NH bytes of ph, then NH of pl
           uint8_t* ptile = smem + C::kPOff + slot * C::kPTile + lrow * C::kPAtomRow;
           constexpr int CPA = C::kPAtomRow / 16;
-          if constexpr (NP == 16) {
-            *reinterpret_cast<uint4*>(ptile + ((sg ^ swz_row) << 4)) = make_uint4(hb[0], hb[1], lb[0], lb[1]);
-          } else {
-            uint32_t all[NP / 4];
+          uint32_t all[NP / 4];
 #pragma unroll
-            for (int i = 0; i < NH / 4; ++i) {
-              all[i] = hb[i];
-              all[NH / 4 + i] = lb[i];
-            }
-#pragma unroll
-            for (int i = 0; i < NP / 16; ++i) {
-              const int cc = sg * (NP / 16) + i;
-              *reinterpret_cast<uint4*>(ptile + (cc / CPA) * C::kPAtomBytes + (((cc % CPA) ^ swz_row) << 4)) =
-                  make_uint4(all[4 * i], all[4 * i + 1], all[4 * i + 2], all[4 * i + 3]);
-            }
+          for (int i = 0; i < NH / 4; ++i) {
+            all[i] = hb[i];
+            all[NH / 4 + i] = lb[i];
           }
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&B->pfull[slot]));
+#pragma unroll
+          for (int i = 0; i < NP / 16; ++i) {
+            const int cc = sg * (NP / 16) + i;
+            *reinterpret_cast<uint4*>(ptile + (cc / CPA) * C::kPAtomBytes + (((cc % CPA) ^ swz_row) << 4)) =
+                make_uint4(all[4 * i], all[4 * i + 1], all[4 * i + 2], all[4 * i + 3]);
+          }
         }
-        if (!ok) break;
+        if (!ok) {
+          tmem_wait_ld();   // nothing in flight when the tensor memory goes away
+          break;
+        }
+        publish((gs + nt - 1) % C::kPT);
         if (lane == 0) mbar_arrive(smem_u32(&B->sm_done[n & 1]));
         gs += nt;
         // the previous chunk's O (its PV has had this chunk's passes to finish)
@@ -887,45 +976,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         {
-          const float r = ColReduce<NH>::run(lsum, lane, 0.f, [](float a, float b) { return a + b; });
-          const int c = ColReduce<NH>::col_of(lane);
-          if (c < NH) redL[(sg * 4 + q4) * NH + c] = r;
-        }
-        if (!wg_sync()) {
-          ok = false;
-          break;
-        }
-        if (gt < NH) {
-          float l = 0.f;
+          float ls[NH];
 #pragma unroll
-          for (int w = 0; w < 4; ++w) l += redL[(sg * 4 + w) * NH + gt];
-          const float ov = vmax * (1.f / 256.f);
-          float a = 0.f, b = ov;
-          if (first) {
-            mrun = mc;
-            lrun = l;
-          } else {
-            const float mn = fmaxf(mrun, mc);
-            a = mrun == -INFINITY ? 0.f : exp2f(mrun - mn);
-            const float bb = mc == -INFINITY ? 0.f : exp2f(mc - mn);
-            b = bb * ov;
-            lrun = lrun * a + l * bb;
-            mrun = mn;
-          }
-          const int k = (n & 1) * NP + c0 + gt;
-          fa[k] = a;
-          fb[k] = b;
-          rm[k] = mrun;
-          rl[k] = lrun;
+          for (int j = 0; j < NH; ++j) ls[j] = (j & 1) ? lsum[j / 2].y : lsum[j / 2].x;
+          const float r = ColReduce<NH>::run(ls, lane, 0.f, [](float a, float b) { return a + b; });
+          const int c = ColReduce<NH>::col_of(lane);
+          if (c < NH) redL[((n & 1) * 8 + sg * 4 + q4) * NH + c] = r;
         }
-        // (visible to the group at the next chunk's barriers, before the epilogue that reads them)
         xp = x;
         pfirst = first;
         plast = last;
       }
     }
-    if (ok && n > 0 && !aborted(abort_flag)) {
-      if (wg_sync()) epilogue(n - 1, xp, pfirst, plast);
+    if (ok && n > 0 && !aborted(abort_flag) && wg_sync()) {
+      join(n - 1);
+      __syncwarp();
+      epilogue(n - 1, xp, pfirst, plast);
     }
   }
 
