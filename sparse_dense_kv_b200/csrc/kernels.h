@@ -122,7 +122,8 @@ struct VerifyKv8Params {
   const int32_t* page_table;
   int max_pages;
   int cap;                 // 16 * max_pages
-  int Hq, Hkv, G, T, R, Rp;
+  int Hq, Hkv, G, T, R;
+  int ngroups, Rg, Rp;     // row groups, rows of one (the last may have fewer), rows of a record
   int64_t num_pages;
   const float* k_scale;
   const float* v_scale;
@@ -256,7 +257,8 @@ int launch_verify_kv8(const CUtensorMap& k1, const CUtensorMap& v1, const CUtens
                       const CUtensorMap& v8, const VerifyKv8Params& p, int D, int batch, int num_sms,
                       cudaStream_t stream, int* launches);
 size_t verify_kv8_bytes(int num_requests, int Hkv, int R, int D, int num_sms);
-int verify_kv8_rec_rows(int R);
+int verify_kv8_groups(int R);
+int verify_kv8_rec_rows(int Rg);
 int verify_kv8_plan_bytes();
 
 int launch_draft_kv8(const DraftKv8Params& p, int D, int batch, cudaStream_t stream);

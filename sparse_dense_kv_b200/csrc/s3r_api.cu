@@ -613,8 +613,11 @@ size_t s3r_kv8_workspace_size(const s3r_kv8_cache* cache, int32_t num_requests, 
   const s3r_kv_cache* c = &cache->pools;
   const int cap = max_pages_per_req * S3R_PAGE_SIZE, sms = sm_count();
   const int G = c->num_q_heads / c->num_kv_heads;
-  const int rows = G * (max_k + 1) < S3R_MAX_ROWS ? G * (max_k + 1) : S3R_MAX_ROWS;
-  size_t part = verify_kv8_bytes(num_requests, c->num_kv_heads, rows, c->head_dim, sms);
+  size_t part = 0;
+  for (int k = 0; k <= max_k && G * (k + 1) <= S3R_MAX_ROWS; ++k) {   // more rows need not mean more bytes
+    const size_t a = verify_kv8_bytes(num_requests, c->num_kv_heads, G * (k + 1), c->head_dim, sms);
+    if (a > part) part = a;
+  }
   const size_t b = draft_kv8_bytes(num_requests, c->num_kv_heads, sel_stride, c->head_dim, sms);
   const size_t d = select_sigma_bytes(num_requests, c->num_kv_heads, cap);
   const size_t e = sample_partial_bytes(num_requests, max_k, vocab > 0 ? vocab : 1);
@@ -698,7 +701,9 @@ int s3r_verify_attn_kv8(const s3r_kv8_cache* cache, const s3r_batch* batch, int3
   p.G = G;
   p.T = k + 1;
   p.R = R;
-  p.Rp = verify_kv8_rec_rows(R);
+  p.ngroups = verify_kv8_groups(R);
+  p.Rg = (R + p.ngroups - 1) / p.ngroups;
+  p.Rp = verify_kv8_rec_rows(p.Rg);
   p.num_pages = c->num_pages;
   p.k_scale = cache->k_scale;
   p.v_scale = cache->v_scale;

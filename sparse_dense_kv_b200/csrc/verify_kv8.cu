@@ -14,35 +14,40 @@
 //   q 2^-e = qh + ql, qh = e4m3(q 2^-e), ql = e4m3(q 2^-e - qh), the row's largest element
 //     scaled to [128, 256): a bf16 value has 8 significant bits and each part holds 4, so the
 //     split is exact down to 2^-10 of the row's largest element and off by at most 2^-18 of it
-//     below. Both parts accumulate into the same S (8 MMAs of K = 32 per tile at d = 128).
-//   p = 2^(x - m) vs / vsmax, the row's reference m (log2 units) such that its largest p of the
-//     chunk is 256: m = max(x + log2(vs / vsmax)) - 8, so a weight keeps its precision next to
-//     what it contributes to the output, however far the page scales are apart. ph = e4m3(p),
-//     pl = e4m3(16 (p - ph)): within 2^-9 of p (bf16's half step is 2^-9 of the next power of
-//     two), and within 2^-22 of the largest p below the normal range. The two parts stand side by
-//     side along N (2 NP columns), so a tile takes 4 MMAs; an MMA of M = 128, K = 32 takes about
-//     70 cycles at N = 32 and at N = 64 alike (measured), so the wider product costs no more.
+//     below.
+//   p = 2^(x - m) vs / vref, the row's reference m (log2 units) such that the largest p so far is
+//     256: m = max(x + log2(vs / vref)) - 8 (vref: the largest V scale of the span's first chunk),
+//     so a weight keeps its precision next to what it contributes to the output, whatever the page
+//     scales are (up to 2^64 apart within a span). ph = e4m3(p),
+//     pl = e4m3(32 (p - ph)): within 2^-9 of p (bf16's half step is 2^-9 of the next power of
+//     two), and within 2^-23 of the largest p below the normal range.
+// The two parts stand side by side along N in both products (2 NP columns): an MMA of M = 128,
+// K = 32 takes 70 to 100 cycles at N = 32 and at N = 64 alike (measured), and the tensor pipe is
+// what a tile's 12 MMAs (both parts into one S) were waiting for; with 8 the softmax is.
 // The scales enter in fp32: ks times the logit of its position (one tensor-memory lane = one
-// position = one page), vs / vsmax of the chunk into p, vsmax into the chunk's O. The row sums are
-// those of 2^(x - m) in fp32; m need not be the row's maximum (it is at least that - 72).
+// position = one page), vs / vref into p, vref into O. The row sums are those of 2^(x - m) in fp32;
+// m need not be the row's maximum (it is within 72 of it).
 //
 // Organisation: one persistent CTA per SM. A work item is a span of consecutive tiles of 128
-// positions of one (request, KV head); spans are claimed from a counter in the workspace. A span
-// is walked in chunks of up to kMT tiles, whose logits stay in tensor memory for an exact
-// two-pass softmax; the chunks of a span are joined in registers (running max and sum), the
-// spans of a (request, KV head) by a second kernel. The span length follows from the launch's
-// total number of tiles: about 6 spans per CTA when there is much to read, so that the claims
-// balance the SMs while the span records stay a few per cent of the traffic; with little to read,
-// 2 spans per CTA down to single tiles, so that a few long requests use every SM.
+// positions of one (request, KV head, row group); more than 32 rows are two groups of half the rows,
+// neighbouring items, so that the second one's K and V come from L2. Spans are claimed from a
+// counter in the workspace. A span is walked in chunks of up to kMT tiles: the first pass joins the
+// two parts of S, applies scales and masks, keeps the logits x in tensor memory and takes the
+// chunk's maxima; the second forms p. Chunks of a span are joined in registers under a running
+// reference, the spans of a (request, KV head) by a second kernel. The span length follows from the
+// launch's total number of tiles: about 6 spans per CTA when there is much to read, so that the
+// claims balance the SMs while the span records stay a few per cent of the traffic; with little to
+// read, 2 spans per CTA down to single tiles, so that a few long requests use every SM.
 //   warp 0     claims spans, streams K tiles (2 KB per page, one TMA box of 16 KB when the 8
 //              pages of a tile are consecutive), publishes each chunk's page scales
 //   warp 1     streams V tiles, zeroing the rows behind the context's end (0 x NaN is NaN), and
 //              splits each span's q rows into the K-major operand while the span before it streams
 //              (a warp of its own would cost the softmax warps 40 of their 168 registers)
-//   warp 2     issues S^T tile (128 positions x NP) = K . [qh, ql]^T, a ring of kNS tiles in
+//   warp 2     issues S^T tile (128 positions x 2 NP) = K . [qh, ql]^T, a ring of kNS tiles in
 //              tensor memory
 //   warp 3     issues O^T (128 d x 2 NP) += V^T . [ph, pl]^T, a ring of kPT tiles of P^T
-//   warps 4-11 softmax, two warpgroups of half the rows each, one thread per position
+//   warps 4-11 softmax, two warpgroups of half the rows each (2 RP rows, the template parameter: no
+//              arithmetic on padding), one thread per position
 // All rings hand over tile by tile. Every wait is bounded (S3R_ERR_TIMEOUT, as in verify_tc.cu).
 #include "kernels.h"
 #include "kv8.cuh"
@@ -59,7 +64,7 @@ constexpr int kSoftWarp0 = 4;
 constexpr int kTileBytes = kPos * 128;    // 16 KB: 128 positions x 128 bytes (d = 64: half zero)
 constexpr int kRing = 16;
 constexpr int kScaleBufs = 4;             // chunks whose page scales are held
-constexpr int kScaleFloats = 196;         // ks, vs / vsmax, log2 of that (>= -64) [64] each; vsmax; pad
+constexpr int kScaleFloats = 196;         // ks, vs / vref, log2 of that (>= -64) [64] each; vref; pad
 constexpr int kBarBytes = 1792;           // barriers, flags, the ring of spans
 constexpr int kMaxBatch = 256;            // requests per launch (larger batches: several launches)
 // plan area of the workspace (written by the attention kernel for the merge): span length in
@@ -81,33 +86,32 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint6
       : "memory");
 }
 
-template <int NP>
+// RP: pairs of rows per warpgroup (1..8).
+template <int RP>
 struct Cfg {
-  // Tensor memory (512 columns): two O buffers of 2 NP columns, then the S ring. A chunk's tiles
-  // must all be resident between the softmax's two passes (kMT <= kNS); what the ring holds
-  // beyond a chunk lets the next chunk's QK run during this chunk's second pass.
-  static constexpr int kOCols = 2 * NP;
-  static constexpr int kSCol0 = 2 * kOCols;
-  static constexpr int kNS = NP == 16 ? 24 : (NP == 32 ? 12 : (NP == 48 ? 6 : 4));
-  static constexpr int kMT = NP <= 32 ? 8 : (NP == 48 ? 5 : 3);   // tiles per chunk
-  static_assert(kSCol0 + kNS * NP <= 512 && kMT <= kNS && kMT <= 8, "tensor memory budget");
-  static constexpr int kPRow = 2 * NP;                            // bytes of P^T per position
+  static constexpr int NP = RP <= 4 ? 16 : 32;   // padded rows
+  static constexpr int NH = NP / 2;              // columns of a warpgroup's part
+  static constexpr int NR = 2 * RP;              // rows of a warpgroup
+  // Tensor memory (512 columns): two O buffers of 2 NP columns, the S ring (2 NP columns per tile:
+  // per warpgroup NH of qh, NH of ql), the logits of a chunk (NP columns per tile).
+  static constexpr int kNS = NP == 16 ? 8 : 2;
+  static constexpr int kMT = 8;                  // tiles per chunk
+  static constexpr int kSCol0 = 4 * NP;
+  static constexpr int kXCol0 = kSCol0 + kNS * 2 * NP;
+  static_assert(kXCol0 + kMT * NP <= 512 && kMT <= 8, "tensor memory budget");
+  static constexpr int kPRow = 2 * NP;           // bytes of P^T per position: 32- or 64-byte swizzle
   static constexpr int kPTile = kPos * kPRow;
-  static constexpr int kPT = 4;                                   // P^T ring
-  static constexpr int kKSt = NP <= 32 ? 5 : (NP == 48 ? 4 : 3);  // K ring stages
-  static constexpr int kVSt = NP <= 32 ? 5 : (NP == 48 ? 4 : 3);  // V ring stages
-  // P^T swizzle: 32-byte rows at 16 rows; 64 at 32; 128 at 64; three 32-byte atoms at 48
-  static constexpr uint32_t kPSwz = (NP == 16 || NP == 48) ? 6u : (NP == 32 ? 4u : 2u);
-  static constexpr int kPAtomRow = (NP == 16 || NP == 48) ? 32 : kPRow;   // bytes of one atom's row
-  static constexpr int kPAtomBytes = kPos * kPAtomRow;
-  static constexpr int kQBytes = 2 * NP * 128;                    // one Q buffer: [h, l][NP rows][128 B]
+  static constexpr uint32_t kPSwz = NP == 16 ? 6u : 4u;
+  static constexpr int kPT = 4;                  // P^T ring
+  static constexpr int kKSt = 5, kVSt = 5;       // K and V ring stages
+  static constexpr int kQBytes = 2 * NP * 128;   // one Q buffer: 2 NP rows of 128 bytes
   static constexpr int kKOff = 0;
   static constexpr int kVOff = kKSt * kTileBytes;
   static constexpr int kQOff = kVOff + kVSt * kTileBytes;
   static constexpr int kPOff = kQOff + 2 * kQBytes;
   static constexpr int kRedOff = kPOff + kPT * kPTile;
-  // floats: redM, redL [2][8 warps][NH]; per-warp rows [8][5][NH]; rs [4][NP]; scales [4][196]
-  static constexpr int kRedFloats = 2 * 2 * 8 * (NP / 2) + 8 * 5 * (NP / 2) + 4 * NP + kScaleBufs * kScaleFloats;
+  // floats: redM, redL [2][8 warps][NH]; per warp [8][3][NH]; rs [4][NP]; scales [4][196]
+  static constexpr int kRedFloats = 2 * 2 * 8 * NH + 8 * 3 * NH + 4 * NP + kScaleBufs * kScaleFloats;
   static constexpr int kPrefOff = kRedOff + kRedFloats * 4;
   static constexpr int kLenOff = kPrefOff + (kMaxBatch + 4) * 4;
   static constexpr int kRidOff = kLenOff + kMaxBatch * 4;
@@ -118,16 +122,16 @@ struct Cfg {
   static_assert(kQOff % 1024 == 0 && kPOff % 1024 == 0 && kRedOff % 16 == 0, "operand alignment");
 };
 
-// A span of tiles [t0, t1) of (request r, KV head kvh), one of nsp; L committed positions.
-// id < 0: the launch has no more work.
+// A span of tiles [t0, t1) of (request r, KV head kvh), one of nsp, for the row group from g0; L
+// committed positions. id < 0: the launch has no more work.
 struct Span {
-  int id, r, kvh, nsp, L, t0, t1, pad;
+  int id, r, kvh, nsp, L, t0, t1, g0;
 };
 
 struct Bars {
   uint64_t kfull[5], kempty[5], ktma[5];
   uint64_t vfull[5], vempty[5], vtma[5];
-  uint64_t sfull[24], sempty[24];
+  uint64_t sfull[8], sempty[8];
   uint64_t pfull[4], pfree[4];
   uint64_t q_full[2], q_empty[2];        // per span parity
   uint64_t qk_done[2], sm_done[2];       // per chunk parity: QK complete; softmax's second pass complete
@@ -144,7 +148,7 @@ struct Bars {
 static_assert(sizeof(Bars) <= kBarBytes && sizeof(Span) == 32, "barrier block");
 
 __device__ __forceinline__ Span make_span(int id, const int* pref, const int* lens_s, const int* rid_s,
-                                          int batch, int Hkv, int T, int st) {
+                                          int batch, const VerifyKv8Params& p, int st) {
   int lo = 0, hi = batch;   // largest b with pref[b] <= id
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -154,22 +158,23 @@ __device__ __forceinline__ Span make_span(int id, const int* pref, const int* le
   Span x;
   x.id = id;
   const int rem = id - pref[lo];
-  x.nsp = (pref[lo + 1] - pref[lo]) / Hkv;
-  x.kvh = rem / x.nsp;
+  x.nsp = (pref[lo + 1] - pref[lo]) / (p.Hkv * p.ngroups);
+  const int pair = rem / p.ngroups;
+  x.g0 = (rem - pair * p.ngroups) * p.Rg;
+  x.kvh = pair / x.nsp;
   x.r = rid_s[lo];
   x.L = lens_s[lo];
-  x.t0 = (rem - x.kvh * x.nsp) * st;
-  x.t1 = min(x.t0 + st, (x.L + T + kPos - 1) / kPos);
-  x.pad = 0;
+  x.t0 = (pair - x.kvh * x.nsp) * st;
+  x.t1 = min(x.t0 + st, (x.L + p.T + kPos - 1) / kPos);
   return x;
 }
 
 // Reduce v[0..N-1] over the warp's lanes with `op`, halving the values at each exchange instead
-// of reducing each one by itself (N = 16: 16 shuffles, not 80). Lane l ends up with the result
+// of reducing each one by itself (N = 14: 16 shuffles, not 70). Lane l ends up with the result
 // of column col_of(l), the same one in every lane that shares it.
 template <int N>
 struct ColReduce {
-  static constexpr int NP2 = N <= 8 ? 8 : (N <= 16 ? 16 : 32);   // N = 24 is padded to 32
+  static constexpr int NP2 = N <= 2 ? 2 : (N <= 4 ? 4 : (N <= 8 ? 8 : 16));   // padded to a power of two
   // column that lane l holds after run()
   __device__ __forceinline__ static int col_of(int lane) {
     int c = 0;
@@ -206,26 +211,46 @@ __device__ __forceinline__ void tmem_tie(float (&v)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
 }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+// This warp's 32 lanes x 8 or 16 consecutive columns.
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const float (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr),
+               "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+               "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
+               "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7]))
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const float (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(taddr),
+      "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+      "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
+      "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])), "r"(__float_as_uint(v[8])),
+      "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])),
+      "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])),
+      "r"(__float_as_uint(v[15]))
+      : "memory");
+}
 template <int N>
 __device__ __forceinline__ void tmem_ready(float (&v)[N]) {
   tmem_wait_ld();
   tmem_tie(v);
 }
 
-template <int NP, int D>
+template <int RP, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     verify_kv8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const __grid_constant__ CUtensorMap tmK8, const __grid_constant__ CUtensorMap tmV8,
                       const VerifyKv8Params p, int batch) {
   pdl_wait();
-  using C = Cfg<NP>;
-  constexpr int NH = NP / 2;
+  using C = Cfg<RP>;
+  constexpr int NP = C::NP, NH = C::NH, NR = C::NR;
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
   float* redM = reinterpret_cast<float*>(smem + C::kRedOff);   // [2][8][NH] warp maxima (chunk parity)
   float* redL = redM + 2 * 8 * NH;                              // [2][8][NH] warp sums
-  float* own = redL + 2 * 8 * NH;                               // [8][5][NH] per warp: max, a, b, run max, run sum
-  float* rs = own + 8 * 5 * NH;                                 // [4][NP] q row factor 2^e / sqrt(d)
+  float* own = redL + 2 * 8 * NH;                               // [8][3][NH] per warp: -reference, O factor (chunk parity)
+  float* rs = own + 8 * 3 * NH;                                 // [4][NP] q row factor 2^e log2(e) / sqrt(d)
   float* scs = rs + 4 * NP;                                     // [4][196] page scales
   int* pref = reinterpret_cast<int*>(smem + C::kPrefOff);
   int* lens_s = reinterpret_cast<int*>(smem + C::kLenOff);
@@ -235,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = &B->abort_flag;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int T = p.T, G = p.G, R = p.R, Hkv = p.Hkv;
+  const int T = p.T, G = p.G, R = p.R, Hkv = p.Hkv, HG = p.Hkv * p.ngroups;
   const uint32_t sbase = smem_u32(smem);
 
   // ---- set-up: lengths, span length, span prefix, barriers, tensor memory
@@ -296,9 +321,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int b = b0; b < b1; ++b) tiles += pref[b + 1];
 #pragma unroll
     for (int o = 16; o; o >>= 1) tiles += __shfl_xor_sync(kFull, tiles, o);
-    const int st = span_tiles(tiles * Hkv, (int)gridDim.x, C::kMT);
+    const int st = span_tiles(tiles * HG, (int)gridDim.x, C::kMT);
     int local = 0;
-    for (int b = b0; b < b1; ++b) local += Hkv * ((pref[b + 1] + st - 1) / st);
+    for (int b = b0; b < b1; ++b) local += HG * ((pref[b + 1] + st - 1) / st);
     int incl = local;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -307,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     int run = incl - local;
     for (int b = b0; b < b1; ++b) {
-      run += Hkv * ((pref[b + 1] + st - 1) / st);
+      run += HG * ((pref[b + 1] + st - 1) / st);
       pref[b + 1] = run;
     }
     if (lane == 0) {
@@ -330,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!wait_bar(smem_u32(&B->item_bar[slot]), (uint32_t)(m / kRing) & 1u, abort_flag, p.err, p.wait_limit)) return false;
     const int4 a = B->span[slot][0], b = B->span[slot][1];
     x.id = a.x; x.r = a.y; x.kvh = a.z; x.nsp = a.w;
-    x.L = b.x; x.t0 = b.y; x.t1 = b.z;
+    x.L = b.x; x.t0 = b.y; x.t1 = b.z; x.g0 = b.w;
     return x.id >= 0;
   };
   auto waitb = [&](uint64_t* bar, int phase) -> bool {
@@ -353,6 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* empty = is_v ? B->vempty : B->kempty;
     uint64_t* tmab = is_v ? B->vtma : B->ktma;
     int* ids_own = ids_s + (is_v ? 64 : 0);
+    float vref = 1.f;          // (K producer)
     int g = 0;                 // tiles issued
     uint32_t tma_phase = 0;    // bit s: phase of tmab[s]
     bool stop = false;
@@ -420,12 +446,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) v = atomicAdd(p.sched, 1);
         id = __shfl_sync(kFull, v, 0) + (int)gridDim.x;
       }
-      if (id < nitems) x = make_span(id, pref, lens_s, rid_s, batch, Hkv, T, st);
+      if (id < nitems) x = make_span(id, pref, lens_s, rid_s, batch, p, st);
       else x.id = -1;
       if (lane == 0) {
         const int slot = m & (kRing - 1);
         B->span[slot][0] = make_int4(x.id, x.r, x.kvh, x.nsp);
-        B->span[slot][1] = make_int4(x.L, x.t0, x.t1, 0);
+        B->span[slot][1] = make_int4(x.L, x.t0, x.t1, x.g0);
         mbar_arrive(smem_u32(&B->item_bar[slot]));   // release: the span is visible
       }
       __syncwarp();
@@ -434,21 +460,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     // q rows of span m -> buffer m & 1 (V producer), once the QK of span m - 2 has read it
     constexpr int LR = D / 8;          // lanes per row (8 elements each)
     constexpr int RI = 32 / LR;        // rows per pass
-    auto zero_q_padding = [&]() {   // rows R..NP-1 of both parts of both buffers stay zero
-      for (int idx = lane; idx < 4 * (NP - R) * 8; idx += 32) {
-        const int h = idx / ((NP - R) * 8), rem = idx - h * (NP - R) * 8;   // h: buffer * 2 + part
-        *reinterpret_cast<uint4*>(smem + C::kQOff + h * (NP * 128) + (R + (rem >> 3)) * 128 + ((rem & 7) << 4)) =
-            make_uint4(0, 0, 0, 0);
-      }
+    auto zero_q = [&]() {   // rows that no q row fills stay zero
+      for (int idx = lane; idx < 2 * C::kQBytes / 16; idx += 32)
+        *reinterpret_cast<uint4*>(smem + C::kQOff + idx * 16) = make_uint4(0, 0, 0, 0);
     };
     auto split_q = [&](const Span& x, int m) -> bool {
       const int qb = m & 1;
       if (m >= 2 && !waitb(&B->q_empty[qb], (m - 2) >> 1)) return false;
-      for (int j0 = 0; j0 < R; j0 += RI) {
+      const int rows = min(p.Rg, R - x.g0);
+      for (int j0 = 0; j0 < rows; j0 += RI) {
         const int j = j0 + lane / LR, c8 = lane % LR;
         uint4 raw = make_uint4(0, 0, 0, 0);
-        if (j < R) {
-          const int t = j / G, gq = j - t * G;
+        if (j < rows) {
+          const int t = (x.g0 + j) / G, gq = x.g0 + j - t * G;
           raw = *reinterpret_cast<const uint4*>(p.q + (((size_t)x.r * T + t) * p.Hq + x.kvh * G + gq) * D + c8 * 8);
         }
         // largest |q| of the row by its bits (NaN above infinity above every finite value)
@@ -479,17 +503,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           hi[i] = bad ? 0x7f7f7f7fu : hh;
           lo[i] = bad ? 0x7f7f7f7fu : ll;
         }
-        if (j < R) {
-          uint8_t* dst = smem + C::kQOff + qb * C::kQBytes + j * 128 + (((c8 >> 1) ^ (j & 7)) << 4) + (c8 & 1) * 8;
-          *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
-          *reinterpret_cast<uint2*>(dst + NP * 128) = make_uint2(lo[0], lo[1]);
+        if (j < rows) {
+          const int w = j / NR, nh = w * NP + j - w * NR, nl = nh + NH;   // operand rows of the two parts
+          uint8_t* dst = smem + C::kQOff + qb * C::kQBytes + (c8 & 1) * 8;
+          *reinterpret_cast<uint2*>(dst + nh * 128 + (((c8 >> 1) ^ (nh & 7)) << 4)) = make_uint2(hi[0], hi[1]);
+          *reinterpret_cast<uint2*>(dst + nl * 128 + (((c8 >> 1) ^ (nl & 7)) << 4)) = make_uint2(lo[0], lo[1]);
           if (c8 == 0) {
-            rs[(m & 3) * NP + j] = __uint_as_float((uint32_t)(127 + e) << 23) * p.scale;
+            rs[(m & 3) * NP + w * NH + j - w * NR] = __uint_as_float((uint32_t)(127 + e) << 23) * p.scale * kLog2e;
             if (bad) set_error(p.err, S3R_ERR_NONFINITE);
           }
         }
       }
-      for (int j = R + lane; j < NP; j += 32) rs[(m & 3) * NP + j] = 0.f;
+      for (int j = rows + lane; j < 2 * NR; j += 32) rs[(m & 3) * NP + j / NR * NH + j % NR] = 0.f;
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&B->q_full[qb]));
@@ -505,7 +530,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       t1 = min(t0 + C::kMT, x.t1);
       fetch_ids(x, t0, t1, ida, idb);
       if (is_v) {
-        zero_q_padding();
+        zero_q();
+        __syncwarp();
         if (!split_q(x, 0)) stop = true;
       }
     }
@@ -535,15 +561,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         float* sc = scs + (n & (kScaleBufs - 1)) * kScaleFloats;
         va = good_scale(va, p.err);
         vb = good_scale(vb, p.err);
-        const float vmax = warp_max(fmaxf(va, vb));
-        const float vnorm = vmax >= 0x1p-120f ? 1.f / vmax : 0.f;   // smaller scales count as zero
+        if (t0 == x.t0) {   // the span's unit of V scales: the largest of its first chunk
+          const float vmax = warp_max(fmaxf(va, vb));
+          vref = vmax >= 0x1p-120f ? vmax : 1.f;
+        }
+        const float inv = 1.f / vref;
+        const float ra = fminf(va * inv, 0x1p64f), rb = fminf(vb * inv, 0x1p64f);
         sc[lane] = good_scale(ka, p.err);
         sc[lane + 32] = good_scale(kb, p.err);
-        sc[64 + lane] = va * vnorm;
-        sc[64 + lane + 32] = vb * vnorm;
-        sc[128 + lane] = fmaxf(log2f(va * vnorm), -64.f);
-        sc[128 + lane + 32] = fmaxf(log2f(vb * vnorm), -64.f);
-        if (lane == 0) sc[192] = vmax;
+        sc[64 + lane] = ra;
+        sc[64 + lane + 32] = rb;
+        sc[128 + lane] = fmaxf(log2f(ra), -64.f);
+        sc[128 + lane + 32] = fmaxf(log2f(rb), -64.f);
+        if (lane == 0) sc[192] = vref;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&B->sc_full[n & (kScaleBufs - 1)]));
       }
@@ -571,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int q = g - nst > 0 ? g - nst : 0; q < g; ++q) mbar_wait(smem_u32(&full[q % nst]), (q / nst) & 1);
   } else if (warp == 2) {
     // ===================================================================== QK issuer ====
-    constexpr uint32_t kId = idesc_e4m3(kPos, NP, false, false);
+    constexpr uint32_t kId = idesc_e4m3(kPos, 2 * NP, false, false);
     int gk = 0, n = 0;
     bool ok = true;
     for (int m = 0; ok; ++m) {
@@ -595,13 +625,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) {
             const uint32_t kt = sbase + C::kKOff + s * kTileBytes;
             const uint32_t qt = qbuf + (m & 1) * C::kQBytes;
-            const uint32_t sd = tmem + C::kSCol0 + d * NP;
+            const uint32_t sd = tmem + C::kSCol0 + d * 2 * NP;
 #pragma unroll
-            for (int half = 0; half < 2; ++half)
-#pragma unroll
-              for (int kk = 0; kk < D / 32; ++kk)
-                mma_e4m3(sd, sdesc(kt + kk * 32, 16, 1024, 2), sdesc(qt + half * (NP * 128) + kk * 32, 16, 1024, 2),
-                         kId, half + kk > 0 ? 1u : 0u);
+            for (int kk = 0; kk < D / 32; ++kk)
+              mma_e4m3(sd, sdesc(kt + kk * 32, 16, 1024, 2), sdesc(qt + kk * 32, 16, 1024, 2), kId, kk > 0 ? 1u : 0u);
             tc_commit(smem_u32(&B->kempty[s]));
             tc_commit(smem_u32(&B->sfull[d]));
           }
@@ -640,12 +667,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) {
             const uint32_t vt = sbase + C::kVOff + s * kTileBytes;
             const uint32_t pt = pbuf + u * C::kPTile;
-            const uint32_t od = tmem + (n & 1) * C::kOCols;
+            const uint32_t od = tmem + (n & 1) * 2 * NP;
 #pragma unroll
             for (int kk = 0; kk < kPos / 32; ++kk)
               // MN-major operands: strides between atoms along M / N and between groups of 8 positions
               mma_e4m3(od, sdesc(vt + kk * 32 * 128, kTileBytes, 1024, 2),
-                       sdesc(pt + kk * 32 * C::kPAtomRow, C::kPAtomBytes, 8 * C::kPAtomRow, C::kPSwz), kId,
+                       sdesc(pt + kk * 32 * C::kPRow, C::kPTile, 8 * C::kPRow, C::kPSwz), kId,
                        t > t0 || kk > 0 ? 1u : 0u);
             tc_commit(smem_u32(&B->vempty[s]));
             tc_commit(smem_u32(&B->pfree[u]));
@@ -664,11 +691,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int sg = (warp - kSoftWarp0) >> 2;        // warpgroup: rows [sg NH, sg NH + NH)
     const int q4 = warp & 3;                        // tensor-memory lane quarter
     const int lrow = q4 * 32 + lane;                // tile position (S) or d (O) of this thread
-    const int c0 = sg * NH;
-    const bool lead8 = (c0 & 15) == 8;
     const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16);
-    // 16-byte chunk XOR of this position's P^T row (32-, 64-, 128-byte swizzle)
-    const int swz_row = (NP == 16 || NP == 48) ? ((lrow >> 2) & 1) : (NP == 32 ? ((lrow >> 1) & 3) : (lrow & 7));
+    // 16-byte chunk XOR of this position's P^T row (32-, 64-byte swizzle)
+    const int swz_row = NP == 16 ? ((lrow >> 2) & 1) : ((lrow >> 1) & 3);
     uint32_t wg_phase = 0;
     auto wg_sync = [&]() -> bool {   // bounded, unlike bar.sync
       __syncwarp();
@@ -677,103 +702,76 @@ __global__ void __launch_bounds__(kThreads, 1)
       wg_phase ^= 1u;
       return r;
     };
-    constexpr bool kHeld = NH <= 16;   // row constants in registers (24 and 32 rows spill)
-    float* cmw = own + (sg * 4 + q4) * 5 * NH;   // this warp's copies of the group's rows: reference,
-    float* faw = cmw + NH;                       //   factor of the running O, of the chunk's O,
-    float* fbw = faw + NH;                       //   running max and running sum
-    float* rmw = fbw + NH;
-    float* rlw = rmw + NH;
-    float orun[NH];   // running O of the span (this thread's d), relative to the running max
+    float* nmw = own + (sg * 4 + q4) * 3 * NH;   // this warp's copies of the group's rows: -reference,
+    float* faw = nmw + NH;                       //   factor of what came before (by chunk parity)
+    float orun[NR], lsum[NR];   // O of the span (this thread's d) and row sums, relative to the reference
     // Chunk n's O joins the span; with its last chunk the span's record (or, when the span is the
-    // whole context, the output) is written.
-    auto epilogue = [&](int n, const Span& x, bool first, bool last) -> bool {
+    // whole context, the output) is written. mrec: the span's reference of row `lane`.
+    auto epilogue = [&](int n, const Span& x, bool first, bool last, int parity, float ov, float mrec) -> bool {
       if (!waitb(&B->o_full[n & 1], n >> 1)) return false;
       tc_fence_after();
       float o[NP];
-      tmem_ld<NP>(tl + (n & 1) * C::kOCols + sg * NP, o);
+      tmem_ld<NP>(tl + (n & 1) * 2 * NP + sg * NP, o);
       tmem_ready(o);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&B->o_empty[n & 1]));
+      const float* fan = faw + (n & 1) * NH;
 #pragma unroll
-      for (int j = 0; j < NH; j += 4) {
-        const float4 a = *reinterpret_cast<const float4*>(faw + j), b = *reinterpret_cast<const float4*>(fbw + j);
-        const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float v = fmaf(o[NH + j + i], 0.0625f, o[j + i]) * bv[i];
-          orun[j + i] = first ? v : fmaf(orun[j + i], av[i], v);
-        }
+      for (int j = 0; j < NR; ++j) {
+        const float v = fmaf(o[NH + j], 0.03125f, o[j]) * ov;
+        orun[j] = first ? v : fmaf(orun[j], fan[j], v);
       }
       if (!last) return true;
+      const int rows = min(NR, min(p.Rg, R - x.g0) - sg * NR), row0 = x.g0 + sg * NR;
+      const float* rl4 = redL + parity * 8 * NH + sg * 4 * NH;   // sums of the group's warps
       if (x.nsp == 1) {
         if (lrow < D) {
 #pragma unroll
-          for (int j = 0; j < NH; ++j) {
-            const int row = c0 + j;
-            if (row < R) {
-              const int t = row / G, gq = row - t * G;
-              p.out[(((size_t)x.r * T + t) * p.Hq + x.kvh * G + gq) * D + lrow] = __float2bfloat16_rn(orun[j] / rlw[j]);
+          for (int j = 0; j < NR; ++j) {
+            if (j < rows) {
+              const float l = (rl4[j] + rl4[NH + j]) + (rl4[2 * NH + j] + rl4[3 * NH + j]);
+              const int t = (row0 + j) / G, gq = row0 + j - t * G;
+              p.out[(((size_t)x.r * T + t) * p.Hq + x.kvh * G + gq) * D + lrow] = __float2bfloat16_rn(orun[j] / l);
             }
           }
         }
-        if (q4 == 0 && lane < NH && c0 + lane < R) {
-          const int row = c0 + lane, t = row / G, gq = row - t * G;
-          p.lse[((size_t)x.r * T + t) * p.Hq + x.kvh * G + gq] = (rmw[lane] + log2f(rlw[lane])) * kLn2;
+        if (q4 == 0 && lane < rows) {
+          const float l = (rl4[lane] + rl4[NH + lane]) + (rl4[2 * NH + lane] + rl4[3 * NH + lane]);
+          const int row = row0 + lane, t = row / G, gq = row - t * G;
+          p.lse[((size_t)x.r * T + t) * p.Hq + x.kvh * G + gq] = (mrec + log2f(l)) * kLn2;
         }
         return true;
       }
       float* rec = p.part + (size_t)x.id * p.Rp * (D + 2);
       if (lrow < D) {
 #pragma unroll
-        for (int j = 0; j < NH; ++j)
-          if (c0 + j < R) rec[2 * p.Rp + (size_t)(c0 + j) * D + lrow] = orun[j];
+        for (int j = 0; j < NR; ++j)
+          if (j < rows) rec[2 * p.Rp + (size_t)(sg * NR + j) * D + lrow] = orun[j];
       }
-      if (q4 == 0 && lane < NH && c0 + lane < R) {
-        rec[c0 + lane] = rmw[lane];
-        rec[p.Rp + c0 + lane] = rlw[lane];
+      if (q4 == 0 && lane < rows) {
+        rec[sg * NR + lane] = mrec;
+        rec[p.Rp + sg * NR + lane] = (rl4[lane] + rl4[NH + lane]) + (rl4[2 * NH + lane] + rl4[3 * NH + lane]);
       }
       return true;
     };
 
     bool ok = true;
     int n = 0, gs = 0;          // chunk and tile counters
-    // Lane j of every warp of the group keeps row c0 + j: running max and sum of the span, maximum
-    // and V factor of the last chunk. The four warps hold the same values, so one barrier per chunk
-    // (the maxima of this chunk, the sums of the one before) is all they need.
-    float mrun = 0.f, lrun = 0.f, mcp = 0.f, ovp = 0.f;
-    const int jl = lane < NH ? lane : NH - 1;
+    // Lane j of every warp of the group keeps row j's reference; the four warps hold the same
+    // values, so the exchange of the chunk maxima is the one barrier of a chunk.
+    float mrun = 0.f, mrec = 0.f, ovp = 0.f;
+    const int jl = lane < NR ? lane : NR - 1;
     Span xp{};
     bool pfirst = false, plast = false;
-    // chunk n - 1 (its sums complete) joins the running state
-    auto join = [&](int n1) {
-      const float* rl4 = redL + (n1 & 1) * 8 * NH + sg * 4 * NH + jl;
-      const float l = (rl4[0] + rl4[NH]) + (rl4[2 * NH] + rl4[3 * NH]);
-      float a = 0.f, b = ovp;
-      if (pfirst) {
-        mrun = mcp;
-        lrun = l;
-      } else {
-        const float mn = fmaxf(mrun, mcp);
-        a = mrun == -INFINITY ? 0.f : exp2f(mrun - mn);
-        const float bb = mcp == -INFINITY ? 0.f : exp2f(mcp - mn);
-        b = bb * ovp;
-        lrun = lrun * a + l * bb;
-        mrun = mn;
-      }
-      if (lane < NH) {
-        faw[lane] = a;
-        fbw[lane] = b;
-        rmw[lane] = mrun;
-        rlw[lane] = lrun;
-      }
-    };
+    int mpar = 0;               // parity of the span before the current one
     for (int m = 0; ok && !aborted(abort_flag); ++m) {
       Span x;
       if (!ring_span(m, x)) break;
       const int L = x.L, Lc = x.L + T;
-      float* scores = p.scores ? p.scores + ((size_t)x.r * Hkv + x.kvh) * (size_t)R * p.cap : nullptr;
-      const float* rsm = rs + (m & 3) * NP + c0;
+      const int row0 = x.g0 + sg * NR, rows = min(p.Rg, R - x.g0) - sg * NR;
+      float* scores = p.scores ? p.scores + (((size_t)x.r * Hkv + x.kvh) * R + row0) * (size_t)p.cap : nullptr;
+      const float* rsm = rs + (m & 3) * NP + sg * NH;
       for (int t0 = x.t0; t0 < x.t1 && ok; t0 += C::kMT, ++n) {
         const int t1 = min(t0 + C::kMT, x.t1), nt = t1 - t0;
         const bool first = t0 == x.t0, last = t1 == x.t1;
@@ -786,160 +784,131 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float* ksc = scs + (n & (kScaleBufs - 1)) * kScaleFloats + (lrow >> 4);   // + 8 per tile
         const float* vsc = ksc + 64;
         const float* lvc = ksc + 128;
-        const float vmax = scs[(n & (kScaleBufs - 1)) * kScaleFloats + 192];
 
-        // pass 1: committed logits out, per row the maximum of x + log2(vs / vsmax); two tiles per
-        // step up to 16 rows
-        float2 mrow[NH / 2], rs2[kHeld ? NH / 2 : 1];   // maxima; row factors (log2 units)
+        // pass 1: logits x (log2 units, -inf where a row does not see the position) to tensor
+        // memory, committed ones out; per row the maximum of x + log2(vs / vref)
+        float2 mrow[RP], rs2[RP];
 #pragma unroll
-        for (int j = 0; j < NH / 2; ++j) {
+        for (int j = 0; j < RP; ++j) {
           mrow[j] = make_float2(-INFINITY, -INFINITY);
-          if constexpr (kHeld) rs2[j] = make_float2(rsm[2 * j] * kLog2e, rsm[2 * j + 1] * kLog2e);
+          rs2[j] = make_float2(rsm[2 * j], rsm[2 * j + 1]);
         }
-        auto row_factor = [&](int j) -> float2 {   // of rows 2j, 2j + 1
-          if constexpr (kHeld) return rs2[j];
-          else return mul2(*reinterpret_cast<const float2*>(rsm + 2 * j), make_float2(kLog2e, kLog2e));
-        };
-        constexpr int U = kHeld ? 2 : 1;
-        for (int u0 = 0; u0 < nt && ok; u0 += U) {
-          float v[U][NH];
-          const int ul = min(u0 + U, nt) - 1;   // an odd last tile is taken twice
-          if (!waitb(&B->sfull[(gs + ul) % C::kNS], (gs + ul) / C::kNS)) {   // tiles complete in order
+        for (int u = 0; u < nt; ++u) {
+          const int d = (gs + u) % C::kNS;
+          if (!waitb(&B->sfull[d], (gs + u) / C::kNS)) {
             ok = false;
             break;
           }
           tc_fence_after();
+          float v[NP];
+          tmem_ld<NP>(tl + C::kSCol0 + d * 2 * NP + sg * NP, v);
+          tmem_ready(v);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&B->sempty[d]));
+          const int p0 = (t0 + u) * kPos, pos = p0 + lrow;
+          const float ks = ksc[u * 8], lv = lvc[u * 8];
+          const float2 ks2 = make_float2(ks, ks), lv2 = make_float2(lv, lv);
+          float2 y[RP];
 #pragma unroll
-          for (int w = 0; w < U; ++w)
-            tmem_ld_cols<NH>(tl + C::kSCol0 + (gs + min(u0 + w, ul)) % C::kNS * NP + c0, v[w], lead8);
-          tmem_wait_ld();
+          for (int j = 0; j < RP; ++j)
+            y[j] = mul2(mul2(add2(make_float2(v[2 * j], v[2 * j + 1]), make_float2(v[NH + 2 * j], v[NH + 2 * j + 1])), ks2),
+                        rs2[j]);
+          if (scores && pos < L) {
+            // a warp's 32 lanes write 32 consecutive positions of a row, one whole 128-byte line
 #pragma unroll
-          for (int w = 0; w < U; ++w) tmem_tie(v[w]);
-#pragma unroll
-          for (int w = 0; w < U; ++w) {
-            const int u = min(u0 + w, ul);
-            const int p0 = (t0 + u) * kPos, pos = p0 + lrow;
-            const float ks = ksc[u * 8];
-            const float2 ks2 = make_float2(ks, ks);
-            float2 y[NH / 2];
-#pragma unroll
-            for (int j = 0; j < NH / 2; ++j) y[j] = mul2(make_float2(v[w][2 * j], v[w][2 * j + 1]), ks2);
-            if (scores && pos < L && u == u0 + w) {
-              float* srow = scores + (size_t)c0 * p.cap + pos;
-#pragma unroll
-              for (int j = 0; j < NH / 2; ++j) {
-                if (c0 + 2 * j < R) srow[(size_t)(2 * j) * p.cap] = y[j].x * rsm[2 * j];
-                if (c0 + 2 * j + 1 < R) srow[(size_t)(2 * j + 1) * p.cap] = y[j].y * rsm[2 * j + 1];
-              }
-            }
-            const float lv = lvc[u * 8];
-            const float2 lv2 = make_float2(lv, lv);
-#pragma unroll
-            for (int j = 0; j < NH / 2; ++j) y[j] = fma2(y[j], row_factor(j), lv2);
-            if (p0 + kPos > L) {
-              // row sees the position: pos < Lc and pos - L <= t, the row's block row
-              const int r0 = pos < L ? 0 : (pos < Lc ? (pos - L) * G : kPos);   // first row that sees it
-#pragma unroll
-              for (int j = 0; j < NH / 2; ++j) {
-                if (c0 + 2 * j < r0 || c0 + 2 * j >= R) y[j].x = -INFINITY;
-                if (c0 + 2 * j + 1 < r0 || c0 + 2 * j + 1 >= R) y[j].y = -INFINITY;
-              }
-            }
-#pragma unroll
-            for (int j = 0; j < NH / 2; ++j) {
-              mrow[j].x = fmaxf(mrow[j].x, y[j].x);
-              mrow[j].y = fmaxf(mrow[j].y, y[j].y);
+            for (int j = 0; j < RP; ++j) {
+              if (2 * j < rows) scores[(size_t)(2 * j) * p.cap + pos] = y[j].x * kLn2;
+              if (2 * j + 1 < rows) scores[(size_t)(2 * j + 1) * p.cap + pos] = y[j].y * kLn2;
             }
           }
+          if (p0 + kPos > L) {
+            // the first row (of this warpgroup's) that sees the position: pos - L <= its block row
+            const int r0 = pos < L ? 0 : (pos < Lc ? (pos - L) * G - row0 : kPos);
+#pragma unroll
+            for (int j = 0; j < RP; ++j) {
+              if (2 * j < r0) y[j].x = -INFINITY;
+              if (2 * j + 1 < r0) y[j].y = -INFINITY;
+            }
+          }
+          float xs[NH];
+#pragma unroll
+          for (int j = 0; j < NH; ++j) xs[j] = j < NR ? ((j & 1) ? y[j / 2].y : y[j / 2].x) : 0.f;
+          tmem_st(tl + C::kXCol0 + u * NP + sg * NH, xs);
+#pragma unroll
+          for (int j = 0; j < RP; ++j) {
+            const float2 z = add2(y[j], lv2);
+            mrow[j].x = fmaxf(mrow[j].x, z.x);
+            mrow[j].y = fmaxf(mrow[j].y, z.y);
+          }
         }
+        tmem_wait_st();
         if (!ok) break;
         {
-          float mx[NH];
+          float mx[NR];
 #pragma unroll
-          for (int j = 0; j < NH; ++j) mx[j] = (j & 1) ? mrow[j / 2].y : mrow[j / 2].x;
-          const float r = ColReduce<NH>::run(mx, lane, -INFINITY, [](float a, float b) { return fmaxf(a, b); });
-          const int c = ColReduce<NH>::col_of(lane);
-          if (c < NH) redM[((n & 1) * 8 + sg * 4 + q4) * NH + c] = r;
+          for (int j = 0; j < NR; ++j) mx[j] = (j & 1) ? mrow[j / 2].y : mrow[j / 2].x;
+          const float r = ColReduce<NR>::run(mx, lane, -INFINITY, [](float a, float b) { return fmaxf(a, b); });
+          const int c = ColReduce<NR>::col_of(lane);
+          if (c < NR) redM[((n & 1) * 8 + sg * 4 + q4) * NH + c] = r;
         }
         if (!wg_sync()) {
           ok = false;
           break;
         }
-        if (n > 0) join(n - 1);
+        const float vref = scs[(n & (kScaleBufs - 1)) * kScaleFloats + 192];
         {
           const float* m4 = redM + (n & 1) * 8 * NH + sg * 4 * NH + jl;
-          const float mx = fmaxf(fmaxf(m4[0], m4[NH]), fmaxf(m4[2 * NH], m4[3 * NH]));
-          mcp = mx - 8.f;
-          ovp = vmax;
-          if (lane < NH) cmw[lane] = mcp;
+          const float mc = fmaxf(fmaxf(m4[0], m4[NH]), fmaxf(m4[2 * NH], m4[3 * NH])) - 8.f;
+          const float mn = first ? mc : fmaxf(mrun, mc);
+          const float a = first || mrun == -INFINITY ? 0.f : exp2f(mrun - mn);
+          mrun = mn;
+          if (lane < NR) {
+            nmw[lane] = mn == -INFINITY ? 0.f : -mn;   // nothing seen yet: 2^-inf = 0
+            faw[(n & 1) * NH + lane] = a;
+          }
         }
         __syncwarp();
-        float2 nm[kHeld ? NH / 2 : 1], lsum[NH / 2];   // -reference, sums
+        float2 nm[RP];
 #pragma unroll
-        for (int j = 0; j < NH / 2; ++j) {
-          if constexpr (kHeld) nm[j] = make_float2(-cmw[2 * j], -cmw[2 * j + 1]);
-          lsum[j] = make_float2(0.f, 0.f);
-        }
+        for (int j = 0; j < RP; ++j) nm[j] = make_float2(nmw[2 * j], nmw[2 * j + 1]);
+        const float* fan = faw + (n & 1) * NH;
+#pragma unroll
+        for (int j = 0; j < NR; ++j) lsum[j] = first ? 0.f : lsum[j] * fan[j];
 
-        // pass 2: 2^(x - m), its sum in fp32, times vs / vsmax in two e4m3 parts to P^T. The
-        // next tile's logits are on their way while this one is worked on, and a tile's P^T is
-        // handed over once the next one is ready to be stored (its stores have drained by then).
+        // pass 2: 2^(x - m), its sum in fp32, times vs / vref in two e4m3 parts to P^T. The next
+        // tile's logits are on their way while this one is worked on, and a tile's P^T is handed
+        // over once the next one is ready to be stored (its stores have drained by then).
         float v[NH];
-        tmem_ld_cols<NH>(tl + C::kSCol0 + gs % C::kNS * NP + c0, v, lead8);
+        tmem_ld<NH>(tl + C::kXCol0 + sg * NH, v);
         auto publish = [&](int slot) {
           fence_proxy_async();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&B->pfull[slot]));
         };
         for (int u = 0; u < nt; ++u) {
-          tmem_wait_ld();
-          tmem_tie(v);
-          float w[NH];
+          tmem_ready(v);
+          float2 e[RP];
 #pragma unroll
-          for (int j = 0; j < NH; ++j) w[j] = v[j];
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&B->sempty[(gs + u) % C::kNS]));
-          if (u + 1 < nt) tmem_ld_cols<NH>(tl + C::kSCol0 + (gs + u + 1) % C::kNS * NP + c0, v, lead8);
-          const int p0 = (t0 + u) * kPos, pos = p0 + lrow;
-          const float ks = ksc[u * 8], vw = vsc[u * 8];
-          const float2 ks2 = make_float2(ks, ks), vw2 = make_float2(vw, vw);
-          const bool interior = p0 + kPos <= L;
-          const int r0 = interior || pos < L ? 0 : (pos < Lc ? (pos - L) * G : kPos);
-          uint32_t hb[NH / 4], lb[NH / 4];
+          for (int j = 0; j < RP; ++j) e[j] = add2(make_float2(v[2 * j], v[2 * j + 1]), nm[j]);
+          if (u + 1 < nt) tmem_ld<NH>(tl + C::kXCol0 + (u + 1) * NP + sg * NH, v);
+          const float vw = vsc[u * 8];
+          const float2 vw2 = make_float2(vw, vw);
+          uint32_t all[NP / 4];
 #pragma unroll
-          for (int j = 0; j < NH; j += 4) {
-            float2 e[2], mj[2];
-            if constexpr (kHeld) {
-              mj[0] = nm[j / 2];
-              mj[1] = nm[j / 2 + 1];
-            } else {
-              const float4 m4 = *reinterpret_cast<const float4*>(cmw + j);
-              mj[0] = make_float2(-m4.x, -m4.y);
-              mj[1] = make_float2(-m4.z, -m4.w);
-            }
+          for (int j = 0; j < NP / 4; ++j) all[j] = 0;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              e[i] = fma2(mul2(make_float2(w[j + 2 * i], w[j + 2 * i + 1]), ks2), row_factor(j / 2 + i), mj[i]);
-              e[i] = make_float2(ex2(e[i].x), ex2(e[i].y));
-            }
-            if (!interior) {
-              // (a row that sees something of the chunk and still has maximum -inf holds NaN, and keeps it)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const int row = c0 + j + 2 * i;
-                if (row < r0 || row >= R) e[i].x = 0.f;
-                if (row + 1 < r0 || row + 1 >= R) e[i].y = 0.f;
-              }
-            }
-            uint32_t h[2], l[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              lsum[j / 2 + i] = add2(lsum[j / 2 + i], e[i]);
-              split_e4m3x2(mul2(e[i], vw2), h[i], l[i]);
-            }
-            hb[j / 4] = __byte_perm(h[0], h[1], 0x5410);
-            lb[j / 4] = __byte_perm(l[0], l[1], 0x5410);
+          for (int j = 0; j < RP; ++j) {
+            e[j] = make_float2(ex2(e[j].x), ex2(e[j].y));
+            const float2 ls = add2(make_float2(lsum[2 * j], lsum[2 * j + 1]), e[j]);
+            lsum[2 * j] = ls.x;
+            lsum[2 * j + 1] = ls.y;
+            uint32_t h, l;
+            split_e4m3x2(mul2(e[j], vw2), h, l);
+            // this warpgroup's NP bytes of the position's row: NH bytes of ph, then NH of pl
+            uint32_t &hw = all[j / 2], &lw = all[NH / 4 + j / 2];
+            hw = (j & 1) ? __byte_perm(hw, h, 0x5410) : h;
+            lw = (j & 1) ? __byte_perm(lw, l, 0x5410) : l;
           }
           const int gp = gs + u, slot = gp % C::kPT;
           if (u > 0) publish((gp - 1) % C::kPT);
@@ -947,21 +916,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          // this warpgroup's NP bytes of the position's row: NH bytes of ph, then NH of pl
-          uint8_t* ptile = smem + C::kPOff + slot * C::kPTile + lrow * C::kPAtomRow;
-          constexpr int CPA = C::kPAtomRow / 16;
-          uint32_t all[NP / 4];
+          uint8_t* ptile = smem + C::kPOff + slot * C::kPTile + lrow * C::kPRow;
 #pragma unroll
-          for (int i = 0; i < NH / 4; ++i) {
-            all[i] = hb[i];
-            all[NH / 4 + i] = lb[i];
-          }
-#pragma unroll
-          for (int i = 0; i < NP / 16; ++i) {
-            const int cc = sg * (NP / 16) + i;
-            *reinterpret_cast<uint4*>(ptile + (cc / CPA) * C::kPAtomBytes + (((cc % CPA) ^ swz_row) << 4)) =
+          for (int i = 0; i < NP / 16; ++i)
+            *reinterpret_cast<uint4*>(ptile + (((sg * (NP / 16) + i) ^ swz_row) << 4)) =
                 make_uint4(all[4 * i], all[4 * i + 1], all[4 * i + 2], all[4 * i + 3]);
-          }
         }
         if (!ok) {
           tmem_wait_ld();   // nothing in flight when the tensor memory goes away
@@ -971,28 +930,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(smem_u32(&B->sm_done[n & 1]));
         gs += nt;
         // the previous chunk's O (its PV has had this chunk's passes to finish)
-        if (n > 0 && !epilogue(n - 1, xp, pfirst, plast)) {
+        if (n > 0 && !epilogue(n - 1, xp, pfirst, plast, mpar, ovp, mrec)) {
           ok = false;
           break;
         }
-        {
-          float ls[NH];
-#pragma unroll
-          for (int j = 0; j < NH; ++j) ls[j] = (j & 1) ? lsum[j / 2].y : lsum[j / 2].x;
-          const float r = ColReduce<NH>::run(ls, lane, 0.f, [](float a, float b) { return a + b; });
-          const int c = ColReduce<NH>::col_of(lane);
-          if (c < NH) redL[((n & 1) * 8 + sg * 4 + q4) * NH + c] = r;
+        if (last) {
+          const float r = ColReduce<NR>::run(lsum, lane, 0.f, [](float a, float b) { return a + b; });
+          const int c = ColReduce<NR>::col_of(lane);
+          if (c < NR) redL[((m & 1) * 8 + sg * 4 + q4) * NH + c] = r;   // read behind the next barrier
         }
         xp = x;
         pfirst = first;
         plast = last;
+        mpar = m & 1;
+        ovp = vref;
+        mrec = mrun;
       }
     }
-    if (ok && n > 0 && !aborted(abort_flag) && wg_sync()) {
-      join(n - 1);
-      __syncwarp();
-      epilogue(n - 1, xp, pfirst, plast);
-    }
+    if (ok && n > 0 && !aborted(abort_flag) && wg_sync()) epilogue(n - 1, xp, pfirst, plast, mpar, ovp, mrec);
   }
 
   tc_fence_before();
@@ -1025,12 +980,13 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kv8_kernel(const Verif
   const int r = p.req_ids ? p.req_ids[p.req_off + bl] : p.req_off + bl;
   if (r < 0 || r >= p.num_requests) return;      // reported by the attention kernel
   const int b0 = p.plan[1 + bl], b1 = p.plan[2 + bl];
-  const int nsp = (b1 - b0) / p.Hkv;
+  const int nsp = (b1 - b0) / (p.Hkv * p.ngroups);
   if (nsp <= 1) return;                          // no work, or written by the attention kernel
-  const size_t pitch = (size_t)p.Rp * (D + 2);
-  const float* rec = p.part + ((size_t)b0 + (size_t)kvh * nsp) * pitch;
+  const int grp = row / p.Rg, jr = row - grp * p.Rg;   // the records are those of the row's group
+  const size_t one = (size_t)p.Rp * (D + 2), pitch = one * p.ngroups;
+  const float* rec = p.part + ((size_t)b0 + (size_t)kvh * nsp * p.ngroups + grp) * one;
   float M = -INFINITY;
-  for (int s = lane; s < nsp; s += 32) M = fmaxf(M, __ldcg(rec + s * pitch + row));
+  for (int s = lane; s < nsp; s += 32) M = fmaxf(M, __ldcg(rec + s * pitch + jr));
   M = warp_max(M);
   float lsum = 0.f;
   float acc[V];
@@ -1039,13 +995,13 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kv8_kernel(const Verif
   for (int s0 = 0; s0 < nsp; s0 += 32) {
     float w = 0.f, l = 0.f;
     if (s0 + lane < nsp) {
-      const float ms = __ldcg(rec + (s0 + lane) * pitch + row);
-      l = __ldcg(rec + (s0 + lane) * pitch + p.Rp + row);
+      const float ms = __ldcg(rec + (s0 + lane) * pitch + jr);
+      l = __ldcg(rec + (s0 + lane) * pitch + p.Rp + jr);
       w = ms == -INFINITY ? 0.f : exp2f(ms - M);
     }
     lsum = fmaf(w, l, lsum);
     const int cnt = min(32, nsp - s0);
-    const float* o = rec + s0 * pitch + 2 * p.Rp + (size_t)row * D + lane * V;
+    const float* o = rec + s0 * pitch + 2 * p.Rp + (size_t)jr * D + lane * V;
     int u = 0;
     for (; u + 4 <= cnt; u += 4) {
       float x[4][V];
@@ -1078,17 +1034,15 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kv8_kernel(const Verif
 
 }  // namespace kv8
 
-static int verify_kv8_npad(int R) { return R <= 16 ? 16 : (R <= 32 ? 32 : (R <= 48 ? 48 : 64)); }
-
-template <int NP, int D>
+template <int RP, int D>
 static int launch_kv8_t(const CUtensorMap& k1, const CUtensorMap& v1, const CUtensorMap& k8,
                         const CUtensorMap& v8, const VerifyKv8Params& p, int batch, int num_sms,
                         cudaStream_t stream) {
-  using C = kv8::Cfg<NP>;
+  using C = kv8::Cfg<RP>;
   static std::atomic<uint64_t> attr_done{0};
-  if (cuda_status(ensure_smem_attr(kv8::verify_kv8_kernel<NP, D>, C::kSmem, attr_done), "cudaFuncSetAttribute") != S3R_OK)
+  if (cuda_status(ensure_smem_attr(kv8::verify_kv8_kernel<RP, D>, C::kSmem, attr_done), "cudaFuncSetAttribute") != S3R_OK)
     return S3R_ERR_CUDA;
-  launch_pdl(kv8::verify_kv8_kernel<NP, D>, num_sms, kv8::kThreads, C::kSmem, stream, k1, v1, k8, v8, p, batch);
+  launch_pdl(kv8::verify_kv8_kernel<RP, D>, num_sms, kv8::kThreads, C::kSmem, stream, k1, v1, k8, v8, p, batch);
   return cuda_status(cudaGetLastError(), "s3r_verify_attn_kv8");
 }
 
@@ -1097,17 +1051,23 @@ static int launch_kv8_d(const CUtensorMap& k1, const CUtensorMap& v1, const CUte
                         const CUtensorMap& v8, const VerifyKv8Params& p, int batch, int num_sms,
                         cudaStream_t stream) {
   int st;
-  switch (verify_kv8_npad(p.R)) {
-    case 16: st = launch_kv8_t<16, D>(k1, v1, k8, v8, p, batch, num_sms, stream); break;
-    case 32: st = launch_kv8_t<32, D>(k1, v1, k8, v8, p, batch, num_sms, stream); break;
-    case 48: st = launch_kv8_t<48, D>(k1, v1, k8, v8, p, batch, num_sms, stream); break;
-    default: st = launch_kv8_t<64, D>(k1, v1, k8, v8, p, batch, num_sms, stream); break;
+  switch ((p.Rg + 3) / 4) {   // pairs of rows per warpgroup
+    case 1: st = launch_kv8_t<1, D>(k1, v1, k8, v8, p, batch, num_sms, stream); break;
+    case 2: st = launch_kv8_t<2, D>(k1, v1, k8, v8, p, batch, num_sms, stream); break;
+    case 3: st = launch_kv8_t<3, D>(k1, v1, k8, v8, p, batch, num_sms, stream); break;
+    case 4: st = launch_kv8_t<4, D>(k1, v1, k8, v8, p, batch, num_sms, stream); break;
+    case 5: st = launch_kv8_t<5, D>(k1, v1, k8, v8, p, batch, num_sms, stream); break;
+    case 6: st = launch_kv8_t<6, D>(k1, v1, k8, v8, p, batch, num_sms, stream); break;
+    case 7: st = launch_kv8_t<7, D>(k1, v1, k8, v8, p, batch, num_sms, stream); break;
+    default: st = launch_kv8_t<8, D>(k1, v1, k8, v8, p, batch, num_sms, stream); break;
   }
   if (st != S3R_OK) return st;
   dim3 grid((p.R + kv8::kMergeWarps - 1) / kv8::kMergeWarps, p.Hkv, batch);
   launch_pdl(kv8::merge_kv8_kernel<D>, grid, 32 * kv8::kMergeWarps, 0, stream, p, batch);
   return cuda_status(cudaGetLastError(), "s3r_verify_attn_kv8 merge");
 }
+
+int verify_kv8_groups(int R) { return R > 32 ? 2 : 1; }
 
 int launch_verify_kv8(const CUtensorMap& k1, const CUtensorMap& v1, const CUtensorMap& k8,
                       const CUtensorMap& v8, const VerifyKv8Params& p, int D, int batch, int num_sms,
@@ -1127,14 +1087,15 @@ int launch_verify_kv8(const CUtensorMap& k1, const CUtensorMap& v1, const CUtens
 
 // Plan area and span records of one launch (at most kMaxBatch requests): the span length is
 // at least total tiles / (6 spans per SM) (or covers a chunk), so there are at most 6 spans per
-// SM and one more for each (request, KV head).
+// SM and one more for each (request, KV head, row group).
 size_t verify_kv8_bytes(int num_requests, int Hkv, int R, int D, int num_sms) {
   const int nb = num_requests < kv8::kMaxBatch ? num_requests : kv8::kMaxBatch;
-  const size_t spans = (size_t)nb * Hkv + (size_t)kSpansPerCta * num_sms;
-  return kv8::kPlanInts * 4 + align_up(spans * (size_t)verify_kv8_rec_rows(R) * (D + 2) * 4, 256);
+  const int ng = verify_kv8_groups(R);
+  const size_t spans = (size_t)nb * Hkv * ng + (size_t)kSpansPerCta * num_sms;
+  return kv8::kPlanInts * 4 + align_up(spans * (size_t)verify_kv8_rec_rows((R + ng - 1) / ng) * (D + 2) * 4, 256);
 }
 
-int verify_kv8_rec_rows(int R) { return (R + 3) / 4 * 4; }
+int verify_kv8_rec_rows(int Rg) { return (Rg + 3) / 4 * 4; }
 int verify_kv8_plan_bytes() { return kv8::kPlanInts * 4; }
 
 }  // namespace s3r
