@@ -65,6 +65,7 @@ constexpr int kTileBytes = kPos * 128;    // 16 KB: 128 positions x 128 bytes (d
 constexpr int kRing = 16;
 constexpr int kScaleBufs = 4;             // chunks whose page scales are held
 constexpr int kScaleFloats = 196;         // ks, vs / vref, log2 of that (>= -64) [64] each; vref; pad
+constexpr int kMaxSt = 6;                 // ring stages
 constexpr int kBarBytes = 1792;           // barriers, flags, the ring of spans
 constexpr int kMaxBatch = 256;            // requests per launch (larger batches: several launches)
 // plan area of the workspace (written by the attention kernel for the merge): span length in
@@ -77,13 +78,28 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn, bool 
   return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                         uint32_t idesc, uint32_t accumulate) {
+// The MMA with its descriptors' low words (start address / 16 and leading offset), which are all
+// that changes from one to the next: a single thread issues them, and every instruction between
+// two of them costs it four cycles or more. ACC: add to D.
+template <bool ACC>
+__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo,
+                                         uint32_t b_hi, uint32_t idesc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %6, 0;\n mov.b64 a, {%1, %2};\n mov.b64 b, {%3, %4};\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "n"(ACC ? 1 : 0)
       : "memory");
+}
+// wait_bar for a single thread.
+__device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err,
+                                         int limit) {
+  for (int i = 0; i < limit; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 255) == 255 && *abort_flag != 0) return false;
+  }
+  *abort_flag = 1;
+  set_error(err, S3R_ERR_TIMEOUT);
+  return false;
 }
 
 // RP: pairs of rows per warpgroup (1..8).
@@ -94,7 +110,7 @@ struct Cfg {
   static constexpr int NR = 2 * RP;              // rows of a warpgroup
   // Tensor memory (512 columns): two O buffers of 2 NP columns, the S ring (2 NP columns per tile:
   // per warpgroup NH of qh, NH of ql), the logits of a chunk (NP columns per tile).
-  static constexpr int kNS = NP == 16 ? 8 : 2;
+  static constexpr int kNS = NP == 16 ? 4 : 2;
   static constexpr int kMT = 8;                  // tiles per chunk
   static constexpr int kSCol0 = 4 * NP;
   static constexpr int kXCol0 = kSCol0 + kNS * 2 * NP;
@@ -102,8 +118,8 @@ struct Cfg {
   static constexpr int kPRow = 2 * NP;           // bytes of P^T per position: 32- or 64-byte swizzle
   static constexpr int kPTile = kPos * kPRow;
   static constexpr uint32_t kPSwz = NP == 16 ? 6u : 4u;
-  static constexpr int kPT = 4;                  // P^T ring
-  static constexpr int kKSt = 5, kVSt = 5;       // K and V ring stages
+  static constexpr int kKSt = 6, kVSt = 4, kPT = 4;   // K, V and P^T ring stages
+  static_assert(kKSt <= kMaxSt && kVSt == kPT && kNS <= kKSt, "shared completion barriers");
   static constexpr int kQBytes = 2 * NP * 128;   // one Q buffer: 2 NP rows of 128 bytes
   static constexpr int kKOff = 0;
   static constexpr int kVOff = kKSt * kTileBytes;
@@ -129,10 +145,13 @@ struct Span {
 };
 
 struct Bars {
-  uint64_t kfull[5], kempty[5], ktma[5];
-  uint64_t vfull[5], vempty[5], vtma[5];
-  uint64_t sfull[8], sempty[8];
-  uint64_t pfull[4], pfree[4];
+  uint64_t kfull[kMaxSt], ktma[kMaxSt];
+  uint64_t vfull[kMaxSt], vtma[kMaxSt];
+  // One commit per tile and product (a commit costs the issuing thread more than an MMA): QK of the
+  // tile in K stage s is complete (the stage is free, its S is there; S slots are fewer than
+  // stages, so no barrier runs a phase ahead of the softmax); PV of the tile in V stage = P slot s.
+  uint64_t qkd[kMaxSt], pvd[kMaxSt];
+  uint64_t sempty[kMaxSt], pfull[kMaxSt];
   uint64_t q_full[2], q_empty[2];        // per span parity
   uint64_t qk_done[2], sm_done[2];       // per chunk parity: QK complete; softmax's second pass complete
   uint64_t sc_full[kScaleBufs];          // chunk's page scales are in shared memory
@@ -277,22 +296,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int s = 0; s < C::kKSt; ++s) {
       mbar_init(smem_u32(&B->kfull[s]), 1);
-      mbar_init(smem_u32(&B->kempty[s]), 1);
       mbar_init(smem_u32(&B->ktma[s]), 1);
+      mbar_init(smem_u32(&B->qkd[s]), 1);
     }
     for (int s = 0; s < C::kVSt; ++s) {
       mbar_init(smem_u32(&B->vfull[s]), 1);
-      mbar_init(smem_u32(&B->vempty[s]), 1);
       mbar_init(smem_u32(&B->vtma[s]), 1);
-    }
-    for (int s = 0; s < C::kNS; ++s) {
-      mbar_init(smem_u32(&B->sfull[s]), 1);
-      mbar_init(smem_u32(&B->sempty[s]), 8);
-    }
-    for (int s = 0; s < C::kPT; ++s) {
+      mbar_init(smem_u32(&B->pvd[s]), 1);
       mbar_init(smem_u32(&B->pfull[s]), 8);
-      mbar_init(smem_u32(&B->pfree[s]), 1);
     }
+    for (int s = 0; s < C::kNS; ++s) mbar_init(smem_u32(&B->sempty[s]), 8);
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&B->q_full[b]), 1);
       mbar_init(smem_u32(&B->q_empty[b]), 1);
@@ -375,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int nst = is_v ? C::kVSt : C::kKSt;
     const int roff = is_v ? C::kVOff : C::kKOff;
     uint64_t* full = is_v ? B->vfull : B->kfull;
-    uint64_t* empty = is_v ? B->vempty : B->kempty;
+    uint64_t* empty = is_v ? B->pvd : B->qkd;
     uint64_t* tmab = is_v ? B->vtma : B->ktma;
     int* ids_own = ids_s + (is_v ? 64 : 0);
     float vref = 1.f;          // (K producer)
@@ -599,93 +612,95 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // nothing may still be landing in this ring when the CTA exits, also after an abort
     for (int q = g - nst > 0 ? g - nst : 0; q < g; ++q) mbar_wait(smem_u32(&full[q % nst]), (q / nst) & 1);
-  } else if (warp == 2) {
-    // ===================================================================== QK issuer ====
-    constexpr uint32_t kId = idesc_e4m3(kPos, 2 * NP, false, false);
-    int gk = 0, n = 0;
-    bool ok = true;
-    for (int m = 0; ok; ++m) {
-      Span x;
-      if (!ring_span(m, x)) break;
-      if (!waitb(&B->q_full[m & 1], m >> 1)) break;
-      for (int t0 = x.t0; t0 < x.t1 && ok; t0 += C::kMT, ++n) {
-        // at most two chunks ahead of the softmax (per-chunk buffers)
-        if (n >= 2 && !waitb(&B->sm_done[n & 1], (n - 2) >> 1)) {
-          ok = false;
-          break;
-        }
-        const int t1 = min(t0 + C::kMT, x.t1);
-        for (int t = t0; t < t1; ++t, ++gk) {
-          const int s = gk % C::kKSt, d = gk % C::kNS;
-          if (!waitb(&B->kfull[s], gk / C::kKSt) || (gk >= C::kNS && !waitb(&B->sempty[d], gk / C::kNS - 1))) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          if (lane == 0) {
-            const uint32_t kt = sbase + C::kKOff + s * kTileBytes;
-            const uint32_t qt = qbuf + (m & 1) * C::kQBytes;
-            const uint32_t sd = tmem + C::kSCol0 + d * 2 * NP;
+  } else if (warp <= 3) {
+    // ==================================================================== MMA issuers ====
+    // Warp 2: QK, warp 3: PV, one thread each.
+    if (lane == 0) {
+      auto wait1 = [&](uint64_t* bar, int phase) -> bool {
+        return wait_one(smem_u32(bar), (uint32_t)phase & 1u, abort_flag, p.err, p.wait_limit);
+      };
+      auto ring1 = [&](int m, Span& x) -> bool {
+        const int slot = m & (kRing - 1);
+        if (!wait1(&B->item_bar[slot], m / kRing)) return false;
+        x.id = B->span[slot][0].x;
+        x.t0 = B->span[slot][1].y;
+        x.t1 = B->span[slot][1].z;
+        return x.id >= 0;
+      };
+      bool ok = true;
+      int g = 0, n = 0;   // tiles, chunks
+      if (warp == 2) {
+        constexpr uint32_t kId = idesc_e4m3(kPos, 2 * NP, false, false);
+        const uint64_t kd = sdesc(sbase + C::kKOff, 16, 1024, 2), qd = sdesc(qbuf, 16, 1024, 2);
+        const uint32_t khi = (uint32_t)(kd >> 32), qhi = (uint32_t)(qd >> 32);
+        for (int m = 0; ok; ++m) {
+          Span x;
+          if (!ring1(m, x) || !wait1(&B->q_full[m & 1], m >> 1)) break;
+          const uint32_t qlo = (uint32_t)qd + (m & 1) * (C::kQBytes >> 4);
+          for (int t0 = x.t0; t0 < x.t1 && ok; t0 += C::kMT, ++n) {
+            // at most two chunks ahead of the softmax (per-chunk buffers)
+            if (n >= 2 && !wait1(&B->sm_done[n & 1], (n - 2) >> 1)) {
+              ok = false;
+              break;
+            }
+            const int t1 = min(t0 + C::kMT, x.t1);
+            for (int t = t0; t < t1; ++t, ++g) {
+              const int s = g % C::kKSt, d = g % C::kNS;
+              if (!wait1(&B->kfull[s], g / C::kKSt) || (g >= C::kNS && !wait1(&B->sempty[d], g / C::kNS - 1))) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const uint32_t klo = (uint32_t)kd + s * (kTileBytes >> 4);
+              const uint32_t sd = tmem + C::kSCol0 + d * 2 * NP;
+              mma_e4m3<false>(sd, klo, khi, qlo, qhi, kId);
 #pragma unroll
-            for (int kk = 0; kk < D / 32; ++kk)
-              mma_e4m3(sd, sdesc(kt + kk * 32, 16, 1024, 2), sdesc(qt + kk * 32, 16, 1024, 2), kId, kk > 0 ? 1u : 0u);
-            tc_commit(smem_u32(&B->kempty[s]));
-            tc_commit(smem_u32(&B->sfull[d]));
+              for (int kk = 1; kk < D / 32; ++kk) mma_e4m3<true>(sd, klo + kk * 2, khi, qlo + kk * 2, qhi, kId);
+              tc_commit(smem_u32(&B->qkd[s]));
+            }
+            if (ok) tc_commit(smem_u32(&B->qk_done[n & 1]));
           }
-          __syncwarp();
+          if (ok) tc_commit(smem_u32(&B->q_empty[m & 1]));
         }
-        if (ok && lane == 0) tc_commit(smem_u32(&B->qk_done[n & 1]));
-        __syncwarp();
-      }
-      if (ok && lane == 0) tc_commit(smem_u32(&B->q_empty[m & 1]));
-      __syncwarp();
-    }
-    if (lane == 0) tc_commit(smem_u32(&B->fin[0]));
-    __syncwarp();
-    mbar_wait(smem_u32(&B->fin[0]), 0);   // not cut short by an abort: the work is in flight
-  } else if (warp == 3) {
-    // ===================================================================== PV issuer ====
-    constexpr uint32_t kId = idesc_e4m3(kPos, 2 * NP, true, true);
-    int gv = 0, n = 0;
-    bool ok = true;
-    for (int m = 0; ok; ++m) {
-      Span x;
-      if (!ring_span(m, x)) break;
-      for (int t0 = x.t0; t0 < x.t1 && ok; t0 += C::kMT, ++n) {
-        if (n >= 2 && !waitb(&B->o_empty[n & 1], (n - 2) >> 1)) {
-          ok = false;
-          break;
-        }
-        const int t1 = min(t0 + C::kMT, x.t1);
-        for (int t = t0; t < t1; ++t, ++gv) {
-          const int s = gv % C::kVSt, u = gv % C::kPT;
-          if (!waitb(&B->pfull[u], gv / C::kPT) || !waitb(&B->vfull[s], gv / C::kVSt)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          if (lane == 0) {
-            const uint32_t vt = sbase + C::kVOff + s * kTileBytes;
-            const uint32_t pt = pbuf + u * C::kPTile;
+      } else {
+        constexpr uint32_t kId = idesc_e4m3(kPos, 2 * NP, true, true);
+        // MN-major operands: strides between atoms along M / N and between groups of 8 positions
+        const uint64_t vd = sdesc(sbase + C::kVOff, kTileBytes, 1024, 2);
+        const uint64_t pd = sdesc(pbuf, C::kPTile, 8 * C::kPRow, C::kPSwz);
+        const uint32_t vhi = (uint32_t)(vd >> 32), phi = (uint32_t)(pd >> 32);
+        for (int m = 0; ok; ++m) {
+          Span x;
+          if (!ring1(m, x)) break;
+          for (int t0 = x.t0; t0 < x.t1 && ok; t0 += C::kMT, ++n) {
+            if (n >= 2 && !wait1(&B->o_empty[n & 1], (n - 2) >> 1)) {
+              ok = false;
+              break;
+            }
             const uint32_t od = tmem + (n & 1) * 2 * NP;
+            const int t1 = min(t0 + C::kMT, x.t1);
+            for (int t = t0; t < t1; ++t, ++g) {
+              const int s = g % C::kVSt;   // V stage and P^T slot
+              if (!wait1(&B->vfull[s], g / C::kVSt) || !wait1(&B->pfull[s], g / C::kPT)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const uint32_t vlo = (uint32_t)vd + s * (kTileBytes >> 4), plo = (uint32_t)pd + s * (C::kPTile >> 4);
+              if (t == t0) mma_e4m3<false>(od, vlo, vhi, plo, phi, kId);
+              else mma_e4m3<true>(od, vlo, vhi, plo, phi, kId);
 #pragma unroll
-            for (int kk = 0; kk < kPos / 32; ++kk)
-              // MN-major operands: strides between atoms along M / N and between groups of 8 positions
-              mma_e4m3(od, sdesc(vt + kk * 32 * 128, kTileBytes, 1024, 2),
-                       sdesc(pt + kk * 32 * C::kPRow, C::kPTile, 8 * C::kPRow, C::kPSwz), kId,
-                       t > t0 || kk > 0 ? 1u : 0u);
-            tc_commit(smem_u32(&B->vempty[s]));
-            tc_commit(smem_u32(&B->pfree[u]));
+              for (int kk = 1; kk < kPos / 32; ++kk)
+                mma_e4m3<true>(od, vlo + kk * (32 * 128 >> 4), vhi, plo + kk * (32 * C::kPRow >> 4), phi, kId);
+              tc_commit(smem_u32(&B->pvd[s]));
+            }
+            if (ok) tc_commit(smem_u32(&B->o_full[n & 1]));
           }
-          __syncwarp();
         }
-        if (ok && lane == 0) tc_commit(smem_u32(&B->o_full[n & 1]));
-        __syncwarp();
       }
+      tc_commit(smem_u32(&B->fin[warp & 1]));
+      mbar_wait(smem_u32(&B->fin[warp & 1]), 0);   // not cut short by an abort: the work is in flight
     }
-    if (lane == 0) tc_commit(smem_u32(&B->fin[1]));
     __syncwarp();
-    mbar_wait(smem_u32(&B->fin[1]), 0);
   } else {
     // ================================================================ softmax warps ====
     const int sg = (warp - kSoftWarp0) >> 2;        // warpgroup: rows [sg NH, sg NH + NH)
@@ -777,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool first = t0 == x.t0, last = t1 == x.t1;
         // the chunk's page scales, and with its first tile the span's row factors
         if (!waitb(&B->sc_full[n & (kScaleBufs - 1)], n / kScaleBufs) ||
-            !waitb(&B->sfull[gs % C::kNS], gs / C::kNS)) {
+            !waitb(&B->qkd[gs % C::kKSt], gs / C::kKSt)) {
           ok = false;
           break;
         }
@@ -795,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int u = 0; u < nt; ++u) {
           const int d = (gs + u) % C::kNS;
-          if (!waitb(&B->sfull[d], (gs + u) / C::kNS)) {
+          if (u > 0 && !waitb(&B->qkd[(gs + u) % C::kKSt], (gs + u) / C::kKSt)) {
             ok = false;
             break;
           }
@@ -912,7 +927,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const int gp = gs + u, slot = gp % C::kPT;
           if (u > 0) publish((gp - 1) % C::kPT);
-          if (gp >= C::kPT && !waitb(&B->pfree[slot], gp / C::kPT - 1)) {
+          if (gp >= C::kPT && !waitb(&B->pvd[slot], gp / C::kPT - 1)) {
             ok = false;
             break;
           }
