@@ -78,27 +78,38 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn, bool 
   return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-// The MMA with its descriptors' low words (start address / 16 and leading offset), which are all
-// that changes from one to the next: a single thread issues them, and every instruction between
-// two of them costs it four cycles or more. ACC: add to D.
+// ACC: add to D. The issuing warp stays converged, its control flow and addresses warp-uniform, and
+// one elected lane executes the MMAs and commits: the operands then come from uniform registers and
+// an MMA leaves every 49 cycles (measured). From a diverged `if (lane == 0)` the same four MMAs and
+// commit took 316 to 450 cycles alone and 800 beside the softmax warps, and the two issuers, each
+// needed by one of the softmax's passes, bounded the kernel.
 template <bool ACC>
-__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo,
-                                         uint32_t b_hi, uint32_t idesc) {
+__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc) {
   asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %6, 0;\n mov.b64 a, {%1, %2};\n mov.b64 b, {%3, %4};\n"
-      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "n"(ACC ? 1 : 0)
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "n"(ACC ? 1 : 0)
       : "memory");
 }
-// wait_bar for a single thread.
-__device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err,
-                                         int limit) {
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n .reg .b32 l;\n elect.sync l|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
+// wait_bar as a loop that stays a loop: inlined some thirty times and unrolled, the waits were most
+// of a 170 KB kernel.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err,
+                                          int limit) {
+#pragma unroll 1
   for (int i = 0; i < limit; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 255) == 255 && *abort_flag != 0) return false;
+    if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
+    if ((i & 255) == 255 && __any_sync(kFull, *abort_flag != 0)) return false;
   }
-  *abort_flag = 1;
-  set_error(err, S3R_ERR_TIMEOUT);
+  if ((threadIdx.x & 31) == 0) {
+    *abort_flag = 1;
+    set_error(err, S3R_ERR_TIMEOUT);
+  }
+  __syncwarp();
   return false;
 }
 
@@ -278,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Bars* B = reinterpret_cast<Bars*>(smem + C::kBarOff);
   volatile int* abort_flag = &B->abort_flag;
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
   const int T = p.T, G = p.G, R = p.R, Hkv = p.Hkv, HG = p.Hkv * p.ngroups;
   const uint32_t sbase = smem_u32(smem);
 
@@ -356,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = B->tmem_base;
+  const uint32_t tmem = __shfl_sync(kFull, B->tmem_base, 0);
   const int nitems = pref[batch], st = B->span_tiles;
   if (blockIdx.x == 0)   // the merge's plan
     for (int b = tid; b <= batch + 1; b += blockDim.x) p.plan[b] = b == 0 ? st : pref[b - 1];
@@ -365,16 +376,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   // claims them and publishes them in a ring (id < 0: no more work).
   auto ring_span = [&](int m, Span& x) -> bool {   // false: no more work, or the wait gave up
     const int slot = m & (kRing - 1);
-    if (!wait_bar(smem_u32(&B->item_bar[slot]), (uint32_t)(m / kRing) & 1u, abort_flag, p.err, p.wait_limit)) return false;
+    if (!wait_warp(smem_u32(&B->item_bar[slot]), (uint32_t)(m / kRing) & 1u, abort_flag, p.err, p.wait_limit)) return false;
     const int4 a = B->span[slot][0], b = B->span[slot][1];
     x.id = a.x; x.r = a.y; x.kvh = a.z; x.nsp = a.w;
     x.L = b.x; x.t0 = b.y; x.t1 = b.z; x.g0 = b.w;
     return x.id >= 0;
   };
   auto waitb = [&](uint64_t* bar, int phase) -> bool {
-    return wait_bar(smem_u32(bar), (uint32_t)phase & 1u, abort_flag, p.err, p.wait_limit);
+    return wait_warp(smem_u32(bar), (uint32_t)phase & 1u, abort_flag, p.err, p.wait_limit);
   };
-  const uint32_t qbuf = sbase + C::kQOff, pbuf = sbase + C::kPOff;
 
   if (warp <= 1) {
     // ============================================================ producers ====
@@ -614,93 +624,105 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int q = g - nst > 0 ? g - nst : 0; q < g; ++q) mbar_wait(smem_u32(&full[q % nst]), (q / nst) & 1);
   } else if (warp <= 3) {
     // ==================================================================== MMA issuers ====
-    // Warp 2: QK, warp 3: PV, one thread each.
-    if (lane == 0) {
-      auto wait1 = [&](uint64_t* bar, int phase) -> bool {
-        return wait_one(smem_u32(bar), (uint32_t)phase & 1u, abort_flag, p.err, p.wait_limit);
-      };
-      auto ring1 = [&](int m, Span& x) -> bool {
-        const int slot = m & (kRing - 1);
-        if (!wait1(&B->item_bar[slot], m / kRing)) return false;
-        x.id = B->span[slot][0].x;
-        x.t0 = B->span[slot][1].y;
-        x.t1 = B->span[slot][1].z;
-        return x.id >= 0;
-      };
-      bool ok = true;
-      int g = 0, n = 0;   // tiles, chunks
-      if (warp == 2) {
-        constexpr uint32_t kId = idesc_e4m3(kPos, 2 * NP, false, false);
-        const uint64_t kd = sdesc(sbase + C::kKOff, 16, 1024, 2), qd = sdesc(qbuf, 16, 1024, 2);
-        const uint32_t khi = (uint32_t)(kd >> 32), qhi = (uint32_t)(qd >> 32);
-        for (int m = 0; ok; ++m) {
-          Span x;
-          if (!ring1(m, x) || !wait1(&B->q_full[m & 1], m >> 1)) break;
-          const uint32_t qlo = (uint32_t)qd + (m & 1) * (C::kQBytes >> 4);
-          for (int t0 = x.t0; t0 < x.t1 && ok; t0 += C::kMT, ++n) {
-            // at most two chunks ahead of the softmax (per-chunk buffers)
-            if (n >= 2 && !wait1(&B->sm_done[n & 1], (n - 2) >> 1)) {
-              ok = false;
-              break;
-            }
-            const int t1 = min(t0 + C::kMT, x.t1);
-            for (int t = t0; t < t1; ++t, ++g) {
-              const int s = g % C::kKSt, d = g % C::kNS;
-              if (!wait1(&B->kfull[s], g / C::kKSt) || (g >= C::kNS && !wait1(&B->sempty[d], g / C::kNS - 1))) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              const uint32_t klo = (uint32_t)kd + s * (kTileBytes >> 4);
-              const uint32_t sd = tmem + C::kSCol0 + d * 2 * NP;
-              mma_e4m3<false>(sd, klo, khi, qlo, qhi, kId);
-#pragma unroll
-              for (int kk = 1; kk < D / 32; ++kk) mma_e4m3<true>(sd, klo + kk * 2, khi, qlo + kk * 2, qhi, kId);
-              tc_commit(smem_u32(&B->qkd[s]));
-            }
-            if (ok) tc_commit(smem_u32(&B->qk_done[n & 1]));
+    // Warp 2: QK, warp 3: PV.
+    auto uni = [](int v) -> int { return __shfl_sync(kFull, v, 0); };
+    const bool el = elect_one();
+    const uint32_t sb = uni((int)sbase), bars = uni((int)smem_u32(B));
+    auto bar_at = [&](const uint64_t* b0, int i) -> uint32_t {
+      return bars + (uint32_t)(reinterpret_cast<const uint8_t*>(b0) - reinterpret_cast<const uint8_t*>(B)) + 8 * i;
+    };
+    bool ok = true;
+    int g = 0, n = 0;   // tiles, chunks
+    if (warp == 2) {
+      constexpr uint32_t kId = idesc_e4m3(kPos, 2 * NP, false, false);
+      const uint64_t kd = sdesc(sb + C::kKOff, 16, 1024, 2), qd = sdesc(sb + C::kQOff, 16, 1024, 2);
+#pragma unroll 1
+      for (int m = 0; ok; ++m) {
+        Span x;
+        if (!ring_span(m, x) || !waitb(&B->q_full[m & 1], m >> 1)) break;
+        const int tb = uni(x.t0), te = uni(x.t1);
+        const uint64_t qm = qd + (m & 1) * (C::kQBytes >> 4);
+#pragma unroll 1
+        for (int t0 = tb; t0 < te && ok; t0 += C::kMT, ++n) {
+          // at most two chunks ahead of the softmax (per-chunk buffers)
+          if (n >= 2 && !waitb(&B->sm_done[n & 1], (n - 2) >> 1)) {
+            ok = false;
+            break;
           }
-          if (ok) tc_commit(smem_u32(&B->q_empty[m & 1]));
-        }
-      } else {
-        constexpr uint32_t kId = idesc_e4m3(kPos, 2 * NP, true, true);
-        // MN-major operands: strides between atoms along M / N and between groups of 8 positions
-        const uint64_t vd = sdesc(sbase + C::kVOff, kTileBytes, 1024, 2);
-        const uint64_t pd = sdesc(pbuf, C::kPTile, 8 * C::kPRow, C::kPSwz);
-        const uint32_t vhi = (uint32_t)(vd >> 32), phi = (uint32_t)(pd >> 32);
-        for (int m = 0; ok; ++m) {
-          Span x;
-          if (!ring1(m, x)) break;
-          for (int t0 = x.t0; t0 < x.t1 && ok; t0 += C::kMT, ++n) {
-            if (n >= 2 && !wait1(&B->o_empty[n & 1], (n - 2) >> 1)) {
+          const int t1 = min(t0 + C::kMT, te);
+#pragma unroll 1
+          for (int t = t0; t < t1; ++t, ++g) {
+            const int s = g % C::kKSt, d = g % C::kNS;
+            if (!waitb(&B->kfull[s], g / C::kKSt) || (g >= C::kNS && !waitb(&B->sempty[d], g / C::kNS - 1))) {
               ok = false;
               break;
             }
-            const uint32_t od = tmem + (n & 1) * 2 * NP;
-            const int t1 = min(t0 + C::kMT, x.t1);
-            for (int t = t0; t < t1; ++t, ++g) {
-              const int s = g % C::kVSt;   // V stage and P^T slot
-              if (!wait1(&B->vfull[s], g / C::kVSt) || !wait1(&B->pfull[s], g / C::kPT)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              const uint32_t vlo = (uint32_t)vd + s * (kTileBytes >> 4), plo = (uint32_t)pd + s * (C::kPTile >> 4);
-              if (t == t0) mma_e4m3<false>(od, vlo, vhi, plo, phi, kId);
-              else mma_e4m3<true>(od, vlo, vhi, plo, phi, kId);
+            tc_fence_after();
+            const uint64_t km = kd + s * (kTileBytes >> 4);
+            const uint32_t sd = tmem + C::kSCol0 + d * 2 * NP, done = bar_at(B->qkd, s);
+            if (el) {
+              mma_e4m3<false>(sd, km, qm, kId);
+#pragma unroll
+              for (int kk = 1; kk < D / 32; ++kk) mma_e4m3<true>(sd, km + kk * 2, qm + kk * 2, kId);
+              tc_commit(done);
+            }
+            __syncwarp();
+          }
+          if (ok && el) tc_commit(bar_at(B->qk_done, n & 1));
+          __syncwarp();
+        }
+        if (ok && el) tc_commit(bar_at(B->q_empty, m & 1));
+        __syncwarp();
+      }
+    } else {
+      constexpr uint32_t kId = idesc_e4m3(kPos, 2 * NP, true, true);
+      // MN-major operands: strides between atoms along M / N and between groups of 8 positions
+      const uint64_t vd = sdesc(sb + C::kVOff, kTileBytes, 1024, 2);
+      const uint64_t pd = sdesc(sb + C::kPOff, C::kPTile, 8 * C::kPRow, C::kPSwz);
+#pragma unroll 1
+      for (int m = 0; ok; ++m) {
+        Span x;
+        if (!ring_span(m, x)) break;
+        const int tb = uni(x.t0), te = uni(x.t1);
+#pragma unroll 1
+        for (int t0 = tb; t0 < te && ok; t0 += C::kMT, ++n) {
+          if (n >= 2 && !waitb(&B->o_empty[n & 1], (n - 2) >> 1)) {
+            ok = false;
+            break;
+          }
+          const uint32_t od = tmem + (n & 1) * 2 * NP;
+          const int t1 = min(t0 + C::kMT, te);
+#pragma unroll 1
+          for (int t = t0; t < t1; ++t, ++g) {
+            const int s = g % C::kVSt;   // V stage and P^T slot
+            if (!waitb(&B->vfull[s], g / C::kVSt) || !waitb(&B->pfull[s], g / C::kPT)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t vm = vd + s * (kTileBytes >> 4), pm = pd + s * (C::kPTile >> 4);
+            const uint32_t done = bar_at(B->pvd, s);
+            if (t == t0) {
+              if (el) mma_e4m3<false>(od, vm, pm, kId);
+            } else {
+              if (el) mma_e4m3<true>(od, vm, pm, kId);
+            }
+            if (el) {
 #pragma unroll
               for (int kk = 1; kk < kPos / 32; ++kk)
-                mma_e4m3<true>(od, vlo + kk * (32 * 128 >> 4), vhi, plo + kk * (32 * C::kPRow >> 4), phi, kId);
-              tc_commit(smem_u32(&B->pvd[s]));
+                mma_e4m3<true>(od, vm + kk * (32 * 128 >> 4), pm + kk * (32 * C::kPRow >> 4), kId);
+              tc_commit(done);
             }
-            if (ok) tc_commit(smem_u32(&B->o_full[n & 1]));
+            __syncwarp();
           }
+          if (ok && el) tc_commit(bar_at(B->o_full, n & 1));
+          __syncwarp();
         }
       }
-      tc_commit(smem_u32(&B->fin[warp & 1]));
-      mbar_wait(smem_u32(&B->fin[warp & 1]), 0);   // not cut short by an abort: the work is in flight
     }
+    if (el) tc_commit(smem_u32(&B->fin[warp & 1]));
     __syncwarp();
+    mbar_wait(smem_u32(&B->fin[warp & 1]), 0);   // not cut short by an abort: the work is in flight
   } else {
     // ================================================================ softmax warps ====
     const int sg = (warp - kSoftWarp0) >> 2;        // warpgroup: rows [sg NH, sg NH + NH)
@@ -713,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto wg_sync = [&]() -> bool {   // bounded, unlike bar.sync
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&B->wg[sg]));
-      const bool r = wait_bar(smem_u32(&B->wg[sg]), wg_phase, abort_flag, p.err, p.wait_limit);
+      const bool r = wait_warp(smem_u32(&B->wg[sg]), wg_phase, abort_flag, p.err, p.wait_limit);
       wg_phase ^= 1u;
       return r;
     };
