@@ -31,24 +31,34 @@
 // Organisation: one persistent CTA per SM. A work item is a span of consecutive tiles of 128
 // positions of one (request, KV head, row group); more than 32 rows are two groups of half the rows,
 // neighbouring items, so that the second one's K and V come from L2. Spans are claimed from a
-// counter in the workspace. A span is walked in chunks of up to kMT tiles: the first pass joins the
-// two parts of S, applies scales and masks, keeps the logits x in tensor memory and takes the
-// chunk's maxima; the second forms p. Chunks of a span are joined in registers under a running
+// counter in the workspace. A span is walked in chunks of up to kMT tiles, in two passes that are two
+// stages of a pipeline, each in warps of its own: the first joins the two parts of S, applies scales
+// and masks, puts the logits x in tensor memory and takes the chunk's maxima; the second forms p from
+// them while the first is at the next chunk. Chunks of a span are joined in registers under a running
 // reference, the spans of a (request, KV head) by a second kernel. The span length follows from the
-// launch's total number of tiles: about 6 spans per CTA when there is much to read, so that the
-// claims balance the SMs while the span records stay a few per cent of the traffic; with little to
-// read, 2 spans per CTA down to single tiles, so that a few long requests use every SM.
-//   warp 0     claims spans, streams K tiles (2 KB per page, one TMA box of 16 KB when the 8
-//              pages of a tile are consecutive), publishes each chunk's page scales
-//   warp 1     streams V tiles, zeroing the rows behind the context's end (0 x NaN is NaN), and
-//              splits each span's q rows into the K-major operand while the span before it streams
-//              (a warp of its own would cost the softmax warps 40 of their 168 registers)
-//   warp 2     issues S^T tile (128 positions x 2 NP) = K . [qh, ql]^T, a ring of kNS tiles in
-//              tensor memory
-//   warp 3     issues O^T (128 d x 2 NP) += V^T . [ph, pl]^T, a ring of kPT tiles of P^T
-//   warps 4-11 softmax, two warpgroups of half the rows each (2 RP rows, the template parameter: no
-//              arithmetic on padding), one thread per position
-// All rings hand over tile by tile. Every wait is bounded (S3R_ERR_TIMEOUT, as in verify_tc.cu).
+// launch's total number of tiles: about 6 spans per CTA when there is much to read, so that the claims
+// balance the SMs while the span records stay a few per cent of the traffic; with little to read, 2
+// spans per CTA down to single tiles, so that a few long requests use every SM.
+//   warp 0      claims spans, streams K tiles (2 KB per page, one TMA box of 16 KB when the 8 pages of
+//               a tile are consecutive), publishes each chunk's page scales, splits the next span's q
+//               rows into the K-major operand
+//   warp 1      streams V tiles, zeroing the rows behind the context's end (0 x NaN is NaN)
+//   warp 2      issues S^T tile (128 positions x 2 NP) = K . [qh, ql]^T, a ring of kNS tiles in
+//               tensor memory
+//   warp 3      issues O^T (128 d x 2 NP) += V^T . [ph, pl]^T, a ring of kPT tiles of P^T
+//   warps 4-7   first pass, one thread per position and all rows
+//   warps 8-15  second pass, two warpgroups of half the rows each (2 RP rows, the template parameter:
+//               no arithmetic on padding), one thread per position
+// Both passes in the same warps, one after the other, left QK idle during the second, PV during the
+// first, and every pipe waiting on one chain (331 us where this takes 303: 32 requests of 8K to
+// 24K tokens, 28 rows, no capture, one B200; 371 with capture; 4 rows 180, 96 % of the measured copy
+// rate, where the softmax is short). What bounds 28 rows is the two
+// passes' instructions, each about 1500 cycles per tile where the copies take 1420, part of it
+// waiting for instructions to be fetched: the size of the code counts, hence the templates and the
+// cold parts out of line. All rings hand over tile by tile. Every wait is bounded
+// (S3R_ERR_TIMEOUT, as in verify_tc.cu).
+#include <type_traits>
+
 #include "kernels.h"
 #include "kv8.cuh"
 #include "tcgen05.cuh"
@@ -59,11 +69,12 @@ namespace kv8 {
 using namespace tc;
 
 constexpr int kPos = 128;
-constexpr int kThreads = 384;
-constexpr int kSoftWarp0 = 4;
+constexpr int kThreads = 512;
+constexpr int kXWarp0 = 4;                // first pass: 4 warps
+constexpr int kPWarp0 = 8;                // second pass: 8 warps
 constexpr int kTileBytes = kPos * 128;    // 16 KB: 128 positions x 128 bytes (d = 64: half zero)
 constexpr int kRing = 16;
-constexpr int kScaleBufs = 4;             // chunks whose page scales are held
+constexpr int kScaleBufs = 8;             // chunks whose page scales are held
 constexpr int kScaleFloats = 196;         // ks, vs / vref, log2 of that (>= -64) [64] each; vref; pad
 constexpr int kMaxSt = 6;                 // ring stages
 constexpr int kBarBytes = 1792;           // barriers, flags, the ring of spans
@@ -96,10 +107,9 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n .reg .pred p;\n .reg .b32 l;\n elect.sync l|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
   return r != 0;
 }
-// wait_bar as a loop that stays a loop: inlined some thirty times and unrolled, the waits were most
-// of a 170 KB kernel.
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err,
-                                          int limit) {
+// wait_bar with its polling out of line: inlined some thirty times, the loops were most of a 170 KB
+// kernel whose warps spent a third of their time waiting for instructions.
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err, int limit) {
 #pragma unroll 1
   for (int i = 0; i < limit; ++i) {
     if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
@@ -112,6 +122,11 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatil
   __syncwarp();
   return false;
 }
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err,
+                                          int limit) {
+  if (__builtin_expect(__all_sync(kFull, mbar_try_wait(bar, parity)), 1)) return true;
+  return wait_slow(bar, parity, abort_flag, err, limit);
+}
 
 // RP: pairs of rows per warpgroup (1..8).
 template <int RP>
@@ -120,12 +135,12 @@ struct Cfg {
   static constexpr int NH = NP / 2;              // columns of a warpgroup's part
   static constexpr int NR = 2 * RP;              // rows of a warpgroup
   // Tensor memory (512 columns): two O buffers of 2 NP columns, the S ring (2 NP columns per tile:
-  // per warpgroup NH of qh, NH of ql), the logits of a chunk (NP columns per tile).
+  // per half of the rows NH of qh, NH of ql), the logits of two chunks (NP columns per tile).
   static constexpr int kNS = NP == 16 ? 4 : 2;
-  static constexpr int kMT = 8;                  // tiles per chunk
+  static constexpr int kMT = NP == 16 ? 8 : 4;   // tiles per chunk
   static constexpr int kSCol0 = 4 * NP;
   static constexpr int kXCol0 = kSCol0 + kNS * 2 * NP;
-  static_assert(kXCol0 + kMT * NP <= 512 && kMT <= 8, "tensor memory budget");
+  static_assert(kXCol0 + 2 * kMT * NP <= 512 && kMT <= 8, "tensor memory budget");
   static constexpr int kPRow = 2 * NP;           // bytes of P^T per position: 32- or 64-byte swizzle
   static constexpr int kPTile = kPos * kPRow;
   static constexpr uint32_t kPSwz = NP == 16 ? 6u : 4u;
@@ -137,13 +152,13 @@ struct Cfg {
   static constexpr int kQOff = kVOff + kVSt * kTileBytes;
   static constexpr int kPOff = kQOff + 2 * kQBytes;
   static constexpr int kRedOff = kPOff + kPT * kPTile;
-  // floats: redM, redL [2][8 warps][NH]; per warp [8][3][NH]; rs [4][NP]; scales [4][196]
-  static constexpr int kRedFloats = 2 * 2 * 8 * NH + 8 * 3 * NH + 4 * NP + kScaleBufs * kScaleFloats;
+  // floats: redM [2][4 warps][NP]; redL [2][8 warps][NH]; references, factors [4][3][NP]; rs [8][NP];
+  // scales [8][196]
+  static constexpr int kRedFloats = 2 * 4 * NP + 2 * 8 * NH + 4 * 3 * NP + 8 * NP + kScaleBufs * kScaleFloats;
   static constexpr int kPrefOff = kRedOff + kRedFloats * 4;
   static constexpr int kLenOff = kPrefOff + (kMaxBatch + 4) * 4;
   static constexpr int kRidOff = kLenOff + kMaxBatch * 4;
-  static constexpr int kIdsOff = kRidOff + kMaxBatch * 4;
-  static constexpr int kBarOff = (kIdsOff + 2 * 64 * 4 + 63) / 64 * 64;
+  static constexpr int kBarOff = (kRidOff + kMaxBatch * 4 + 63) / 64 * 64;
   static constexpr int kSmem = kBarOff + kBarBytes + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
   static_assert(kQOff % 1024 == 0 && kPOff % 1024 == 0 && kRedOff % 16 == 0, "operand alignment");
@@ -164,11 +179,12 @@ struct Bars {
   uint64_t qkd[kMaxSt], pvd[kMaxSt];
   uint64_t sempty[kMaxSt], pfull[kMaxSt];
   uint64_t q_full[2], q_empty[2];        // per span parity
-  uint64_t qk_done[2], sm_done[2];       // per chunk parity: QK complete; softmax's second pass complete
+  uint64_t x_full[2], x_empty[2];        // per chunk parity: its logits are in tensor memory; have been read
+  uint64_t sm_done[kScaleBufs];          // chunk's second pass is over
   uint64_t sc_full[kScaleBufs];          // chunk's page scales are in shared memory
   uint64_t o_full[2], o_empty[2];        // per chunk parity
   uint64_t fin[2];
-  uint64_t wg[2];
+  uint64_t wg[3];                        // the second pass's two warpgroups, the first pass's
   uint64_t item_bar[kRing];
   int4 span[kRing][2];                   // the CTA's m-th span at m % kRing
   uint32_t tmem_base;
@@ -200,11 +216,11 @@ __device__ __forceinline__ Span make_span(int id, const int* pref, const int* le
 }
 
 // Reduce v[0..N-1] over the warp's lanes with `op`, halving the values at each exchange instead
-// of reducing each one by itself (N = 14: 16 shuffles, not 70). Lane l ends up with the result
+// of reducing each one by itself (N = 28: 31 shuffles, not 140). Lane l ends up with the result
 // of column col_of(l), the same one in every lane that shares it.
 template <int N>
 struct ColReduce {
-  static constexpr int NP2 = N <= 2 ? 2 : (N <= 4 ? 4 : (N <= 8 ? 8 : 16));   // padded to a power of two
+  static constexpr int NP2 = N <= 2 ? 2 : (N <= 4 ? 4 : (N <= 8 ? 8 : (N <= 16 ? 16 : 32)));   // padded to a power of two
   // column that lane l holds after run()
   __device__ __forceinline__ static int col_of(int lane) {
     int c = 0;
@@ -267,7 +283,9 @@ __device__ __forceinline__ void tmem_ready(float (&v)[N]) {
   tmem_tie(v);
 }
 
-template <int RP, int D>
+// CAP: committed logits are written (their stores, skipped over, would still cost the other case a
+// tenth of its time in instruction fetches).
+template <int RP, int D, bool CAP>
 __global__ void __launch_bounds__(kThreads, 1)
     verify_kv8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const __grid_constant__ CUtensorMap tmK8, const __grid_constant__ CUtensorMap tmV8,
@@ -277,15 +295,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int NP = C::NP, NH = C::NH, NR = C::NR;
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
-  float* redM = reinterpret_cast<float*>(smem + C::kRedOff);   // [2][8][NH] warp maxima (chunk parity)
-  float* redL = redM + 2 * 8 * NH;                              // [2][8][NH] warp sums
-  float* own = redL + 2 * 8 * NH;                               // [8][3][NH] per warp: -reference, O factor (chunk parity)
-  float* rs = own + 8 * 3 * NH;                                 // [4][NP] q row factor 2^e log2(e) / sqrt(d)
-  float* scs = rs + 4 * NP;                                     // [4][196] page scales
+  float* redM = reinterpret_cast<float*>(smem + C::kRedOff);   // [2][4][NP] warp maxima (chunk parity)
+  float* redL = redM + 2 * 4 * NP;                              // [2][8][NH] warp sums (span parity)
+  float* refs = redL + 2 * 8 * NH;                              // [4][3][NP] chunk & 3: -reference, O factor, reference
+  float* rs = refs + 4 * 3 * NP;                                // [8][NP] q row factor 2^e log2(e) / sqrt(d)
+  float* scs = rs + 8 * NP;                                     // [8][196] page scales
   int* pref = reinterpret_cast<int*>(smem + C::kPrefOff);
   int* lens_s = reinterpret_cast<int*>(smem + C::kLenOff);
   int* rid_s = reinterpret_cast<int*>(smem + C::kRidOff);
-  int* ids_s = reinterpret_cast<int*>(smem + C::kIdsOff);
   Bars* B = reinterpret_cast<Bars*>(smem + C::kBarOff);
   volatile int* abort_flag = &B->abort_flag;
 
@@ -316,18 +333,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&B->pvd[s]), 1);
       mbar_init(smem_u32(&B->pfull[s]), 8);
     }
-    for (int s = 0; s < C::kNS; ++s) mbar_init(smem_u32(&B->sempty[s]), 8);
+    for (int s = 0; s < C::kNS; ++s) mbar_init(smem_u32(&B->sempty[s]), 4);
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&B->q_full[b]), 1);
       mbar_init(smem_u32(&B->q_empty[b]), 1);
-      mbar_init(smem_u32(&B->qk_done[b]), 1);
-      mbar_init(smem_u32(&B->sm_done[b]), 8);
+      mbar_init(smem_u32(&B->x_full[b]), 4);
+      mbar_init(smem_u32(&B->x_empty[b]), 8);
       mbar_init(smem_u32(&B->o_full[b]), 1);
       mbar_init(smem_u32(&B->o_empty[b]), 8);
       mbar_init(smem_u32(&B->fin[b]), 1);
       mbar_init(smem_u32(&B->wg[b]), 4);
     }
-    for (int i = 0; i < kScaleBufs; ++i) mbar_init(smem_u32(&B->sc_full[i]), 1);
+    for (int i = 0; i < kScaleBufs; ++i) {
+      mbar_init(smem_u32(&B->sc_full[i]), 1);
+      mbar_init(smem_u32(&B->sm_done[i]), 8);
+    }
+    mbar_init(smem_u32(&B->wg[2]), 4);
     for (int i = 0; i < kRing; ++i) mbar_init(smem_u32(&B->item_bar[i]), 1);
     B->abort_flag = 0;
     fence_mbar_init();
@@ -374,12 +395,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // A CTA's first span is blockIdx.x, later ones come from the launch's counter; the K producer
   // claims them and publishes them in a ring (id < 0: no more work).
-  auto ring_span = [&](int m, Span& x) -> bool {   // false: no more work, or the wait gave up
-    const int slot = m & (kRing - 1);
-    if (!wait_warp(smem_u32(&B->item_bar[slot]), (uint32_t)(m / kRing) & 1u, abort_flag, p.err, p.wait_limit)) return false;
-    const int4 a = B->span[slot][0], b = B->span[slot][1];
+  auto read_span = [&](int m, Span& x) {
+    const int4 a = B->span[m & (kRing - 1)][0], b = B->span[m & (kRing - 1)][1];
     x.id = a.x; x.r = a.y; x.kvh = a.z; x.nsp = a.w;
     x.L = b.x; x.t0 = b.y; x.t1 = b.z; x.g0 = b.w;
+  };
+  auto ring_span = [&](int m, Span& x) -> bool {   // false: no more work, or the wait gave up
+    if (!wait_warp(smem_u32(&B->item_bar[m & (kRing - 1)]), (uint32_t)(m / kRing) & 1u, abort_flag, p.err, p.wait_limit))
+      return false;
+    read_span(m, x);
     return x.id >= 0;
   };
   auto waitb = [&](uint64_t* bar, int phase) -> bool {
@@ -400,9 +424,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* full = is_v ? B->vfull : B->kfull;
     uint64_t* empty = is_v ? B->pvd : B->qkd;
     uint64_t* tmab = is_v ? B->vtma : B->ktma;
-    int* ids_own = ids_s + (is_v ? 64 : 0);
+    const uint32_t sb = __shfl_sync(kFull, sbase, 0);
     float vref = 1.f;          // (K producer)
-    int g = 0;                 // tiles issued
+    int g = 0, slot = 0, lap = 0;   // tiles issued; the ring's position
     uint32_t tma_phase = 0;    // bit s: phase of tmab[s]
     bool stop = false;
     // Page ids of the chunk [t0, t1), two per lane (-1 past the context or outside the pool).
@@ -412,35 +436,55 @@ __global__ void __launch_bounds__(kThreads, 1)
       a = lane < npg && pg0 + lane < pend ? ptab[pg0 + lane] : -1;
       b = lane + 32 < npg && pg0 + lane + 32 < pend ? ptab[pg0 + lane + 32] : -1;
     };
-    auto load_tile = [&](const Span& x, int t, int i0) {   // i0: the tile's first page in ids_own
-      const int s = g % nst;
-      if (g >= nst && !waitb(&empty[s], g / nst - 1)) {
+    const bool el = elect_one();
+    // The pages of a chunk: which are in the context, which of those are in the pool, which follow
+    // the one before (bit i: page i of the chunk). Found once per chunk; a tile is a byte of each.
+    uint64_t want = 0, good = 0, next = 0;
+    auto survey = [&](const Span& x, int t0, int t1, int ida, int idb) {
+      const int left = (x.L + T + kPage - 1) / kPage - t0 * 8, npg = min(left, (t1 - t0) * 8);
+      auto one = [&](int id, int i, int before) -> void {
+        const bool w = i < npg, g2 = w && id >= 0 && id < p.num_pages;
+        const int sh = i & 32;
+        want |= (uint64_t)__ballot_sync(kFull, w) << sh;
+        good |= (uint64_t)__ballot_sync(kFull, g2) << sh;
+        next |= (uint64_t)__ballot_sync(kFull, id == before + 1) << sh;
+      };
+      want = good = next = 0;
+      one(ida, lane, __shfl_up_sync(kFull, ida, 1));
+      if (C::kMT > 4) one(idb, lane + 32, __shfl_up_sync(kFull, idb, 1));
+      if (want != good && lane == 0) set_error(p.err, S3R_ERR_DEVICE_BOUNDS);
+    };
+    auto load_tile = [&](const Span& x, int t, int u, int ida, int idb) {   // u: tile of the chunk
+      const int s = slot;
+      if (g >= nst && !waitb(&empty[s], lap - 1)) {
         stop = true;
         return;
       }
-      const uint32_t dst = sbase + roff + s * kTileBytes;
-      const int Lc = x.L + T, pend = (Lc + kPage - 1) / kPage;
-      // one page per lane (lanes 0..7)
-      const int pg = t * 8 + lane;
-      const int id = lane < 8 ? ids_own[i0 + lane] : -1;
-      const bool want = lane < 8 && pg < pend;
-      const bool good = want && id >= 0 && id < p.num_pages;
-      if (want && !good) set_error(p.err, S3R_ERR_DEVICE_BOUNDS);
-      const uint32_t okmask = __ballot_sync(kFull, good) & 0xFFu;
-      const uint32_t wantmask = __ballot_sync(kFull, want) & 0xFFu;
-      const int id0 = __shfl_sync(kFull, id, 0);
-      const bool run = __all_sync(kFull, lane >= 8 || (good && id == id0 + lane));
+      if (++slot == nst) {   // (counted: a division by the runtime ring size costs more than the copy)
+        slot = 0;
+        ++lap;
+      }
+      const uint32_t dst = sb + roff + s * kTileBytes;
+      const uint32_t okmask = (uint32_t)(good >> (8 * u)) & 0xFFu, wantmask = (uint32_t)(want >> (8 * u)) & 0xFFu;
+      const bool run = okmask == 0xFFu && ((uint32_t)(next >> (8 * u)) & 0xFEu) == 0xFEu;   // 8 consecutive ids
+      const int Lc = x.L + T;
       // rows that must read as zero: a bad page's, and for V every row behind the context
       const bool patch = okmask != wantmask || (is_v && (t + 1) * kPos > Lc);
       const uint32_t landing = smem_u32(patch ? &tmab[s] : &full[s]);
+      const int id0 = __shfl_sync(kFull, C::kMT > 4 && u >= 4 ? idb : ida, (8 * u) & 31);
+      ++g;
+      if (__builtin_expect(run && !patch, 1)) {
+        if (el) {
+          mbar_arrive_expect_tx(landing, 8 * kPage * 128);
+          tma_load_4d(dst, map8, 0, 0, x.kvh, id0, landing);
+        }
+        __syncwarp();
+        return;
+      }
+      const int id = __shfl_sync(kFull, C::kMT > 4 && u >= 4 ? idb : ida, (8 * u + (lane & 7)) & 31);
       if (lane == 0) mbar_arrive_expect_tx(landing, (uint32_t)__popc(okmask) * kPage * 128);
       __syncwarp();
-      if (run) {
-        if (lane == 0) tma_load_4d(dst, map8, 0, 0, x.kvh, id0, landing);
-      } else if (good) {
-        tma_load_4d(dst + lane * kPage * 128, map, 0, 0, x.kvh, id, landing);
-      }
-      ++g;
+      if (lane < 8 && (okmask & (1u << lane))) tma_load_4d(dst + lane * kPage * 128, map, 0, 0, x.kvh, id, landing);
       if (patch) {
         if (!waitb(&tmab[s], (tma_phase >> s) & 1)) {
           mbar_wait(smem_u32(&tmab[s]), (tma_phase >> s) & 1);   // its copies land before exit
@@ -449,6 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           return;
         }
         tma_phase ^= 1u << s;
+#pragma unroll 1
         for (int idx = lane; idx < kPos * 8; idx += 32) {
           const int row = idx >> 3;
           if ((okmask & (1u << (row >> 4))) && !(is_v && t * kPos + row >= Lc)) continue;
@@ -480,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       return x.id >= 0;
     };
-    // q rows of span m -> buffer m & 1 (V producer), once the QK of span m - 2 has read it
+    // q rows of span m -> buffer m & 1 (K producer), once the QK of span m - 2 has read it
     constexpr int LR = D / 8;          // lanes per row (8 elements each)
     constexpr int RI = 32 / LR;        // rows per pass
     auto zero_q = [&]() {   // rows that no q row fills stay zero
@@ -491,13 +536,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int qb = m & 1;
       if (m >= 2 && !waitb(&B->q_empty[qb], (m - 2) >> 1)) return false;
       const int rows = min(p.Rg, R - x.g0);
-      for (int j0 = 0; j0 < rows; j0 += RI) {
-        const int j = j0 + lane / LR, c8 = lane % LR;
-        uint4 raw = make_uint4(0, 0, 0, 0);
-        if (j < rows) {
-          const int t = (x.g0 + j) / G, gq = x.g0 + j - t * G;
-          raw = *reinterpret_cast<const uint4*>(p.q + (((size_t)x.r * T + t) * p.Hq + x.kvh * G + gq) * D + c8 * 8);
+      constexpr int kAhead = 8;   // loads in flight
+      uint4 rows_raw[kAhead];
+#pragma unroll 1
+      for (int jb = 0; jb < rows; jb += kAhead * RI) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const int j = jb + i * RI + lane / LR, c8 = lane % LR;
+          rows_raw[i] = make_uint4(0, 0, 0, 0);
+          if (j < rows) {
+            const int t = (x.g0 + j) / G, gq = x.g0 + j - t * G;
+            rows_raw[i] = *reinterpret_cast<const uint4*>(p.q + (((size_t)x.r * T + t) * p.Hq + x.kvh * G + gq) * D + c8 * 8);
+          }
         }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int j0 = jb + i * RI;
+        if (j0 >= rows) break;
+        const int j = j0 + lane / LR, c8 = lane % LR;
+        const uint4 raw = rows_raw[i];
         // largest |q| of the row by its bits (NaN above infinity above every finite value)
         uint32_t a = __vmaxu2(__vmaxu2(raw.x & 0x7fff7fffu, raw.y & 0x7fff7fffu),
                               __vmaxu2(raw.z & 0x7fff7fffu, raw.w & 0x7fff7fffu));
@@ -532,12 +589,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<uint2*>(dst + nh * 128 + (((c8 >> 1) ^ (nh & 7)) << 4)) = make_uint2(hi[0], hi[1]);
           *reinterpret_cast<uint2*>(dst + nl * 128 + (((c8 >> 1) ^ (nl & 7)) << 4)) = make_uint2(lo[0], lo[1]);
           if (c8 == 0) {
-            rs[(m & 3) * NP + w * NH + j - w * NR] = __uint_as_float((uint32_t)(127 + e) << 23) * p.scale * kLog2e;
+            rs[(m & 7) * NP + w * NH + j - w * NR] = __uint_as_float((uint32_t)(127 + e) << 23) * p.scale * kLog2e;
             if (bad) set_error(p.err, S3R_ERR_NONFINITE);
           }
         }
       }
-      for (int j = rows + lane; j < 2 * NR; j += 32) rs[(m & 3) * NP + j / NR * NH + j % NR] = 0.f;
+      }
+#pragma unroll 1
+      for (int j = rows + lane; j < 2 * NR; j += 32) rs[(m & 7) * NP + j / NR * NH + j % NR] = 0.f;
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&B->q_full[qb]));
@@ -552,33 +611,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       t0 = x.t0;
       t1 = min(t0 + C::kMT, x.t1);
       fetch_ids(x, t0, t1, ida, idb);
-      if (is_v) {
+      if (!is_v) {
         zero_q();
         __syncwarp();
         if (!split_q(x, 0)) stop = true;
       }
     }
-    while (more && !stop && !aborted(abort_flag)) {
-      __syncwarp();
-      ids_own[lane] = ida;
-      ids_own[lane + 32] = idb;
-      __syncwarp();
-      // page scales of this chunk (K producer): loaded now, stored once the first tile is issued
-      float ka = 0.f, kb = 0.f, va = 0.f, vb = 0.f;
-      if (!is_v) {
-        if (ida >= 0 && ida < p.num_pages) {
-          ka = __ldg(p.k_scale + (size_t)ida * Hkv + x.kvh);
-          va = __ldg(p.v_scale + (size_t)ida * Hkv + x.kvh);
-        }
-        if (idb >= 0 && idb < p.num_pages) {
-          kb = __ldg(p.k_scale + (size_t)idb * Hkv + x.kvh);
-          vb = __ldg(p.v_scale + (size_t)idb * Hkv + x.kvh);
-        }
+    // page scales of the next chunk (K producer), loaded while the current one streams
+    float ka = 0.f, kb = 0.f, va = 0.f, vb = 0.f;
+    auto fetch_scales = [&](const Span& y) {
+      ka = kb = va = vb = 0.f;
+      if (ida >= 0 && ida < p.num_pages) {
+        ka = __ldg(p.k_scale + (size_t)ida * Hkv + y.kvh);
+        va = __ldg(p.v_scale + (size_t)ida * Hkv + y.kvh);
       }
-      // At most two chunks ahead of QK, checked before this chunk's first tile (QK(n) cannot be
-      // over yet): scale buffer n & 3 was read by chunk n - 4, whose softmax is over once QK(n - 2) is.
-      if (!is_v && n >= 2 && !waitb(&B->qk_done[n & 1], (n - 2) >> 1)) break;
-      load_tile(x, t0, 0);
+      if (C::kMT > 4 && idb >= 0 && idb < p.num_pages) {
+        kb = __ldg(p.k_scale + (size_t)idb * Hkv + y.kvh);
+        vb = __ldg(p.v_scale + (size_t)idb * Hkv + y.kvh);
+      }
+    };
+    if (more && !is_v) fetch_scales(x);
+    while (more && !stop && !aborted(abort_flag)) {
+      survey(x, t0, t1, ida, idb);
+      // at most four chunks ahead of the second pass: what the scale buffers and the span ring hold
+      if (!is_v && n >= 4 && !waitb(&B->sm_done[(n - 4) & (kScaleBufs - 1)], (n - 4) / kScaleBufs)) break;
+      load_tile(x, t0, 0, ida, idb);
       if (stop) break;
       if (!is_v) {
         float* sc = scs + (n & (kScaleBufs - 1)) * kScaleFloats;
@@ -610,14 +667,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int nt1 = min(nt0 + C::kMT, xn.t1);
       if (more) {
         fetch_ids(xn, nt0, nt1, na, nb);
-        if (is_v && t1 >= x.t1 && !split_q(xn, m)) stop = true;
+        if (!is_v && t1 >= x.t1 && !split_q(xn, m)) stop = true;
       }
-      for (int t = t0 + 1; t < t1 && !stop; ++t) load_tile(x, t, (t - t0) * 8);
+#pragma unroll 1
+      for (int t = t0 + 1; t < t1 && !stop; ++t) load_tile(x, t, t - t0, ida, idb);
       x = xn;
       t0 = nt0;
       t1 = nt1;
       ida = na;
       idb = nb;
+      if (more && !is_v) fetch_scales(x);
       ++n;
     }
     // nothing may still be landing in this ring when the CTA exits, also after an abort
@@ -634,6 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int g = 0, n = 0;   // tiles, chunks
     if (warp == 2) {
+      int s = 0, lap = 0;   // position in the K ring
       constexpr uint32_t kId = idesc_e4m3(kPos, 2 * NP, false, false);
       const uint64_t kd = sdesc(sb + C::kKOff, 16, 1024, 2), qd = sdesc(sb + C::kQOff, 16, 1024, 2);
 #pragma unroll 1
@@ -643,17 +703,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int tb = uni(x.t0), te = uni(x.t1);
         const uint64_t qm = qd + (m & 1) * (C::kQBytes >> 4);
 #pragma unroll 1
-        for (int t0 = tb; t0 < te && ok; t0 += C::kMT, ++n) {
-          // at most two chunks ahead of the softmax (per-chunk buffers)
-          if (n >= 2 && !waitb(&B->sm_done[n & 1], (n - 2) >> 1)) {
-            ok = false;
-            break;
-          }
+        for (int t0 = tb; t0 < te && ok; t0 += C::kMT) {
           const int t1 = min(t0 + C::kMT, te);
 #pragma unroll 1
           for (int t = t0; t < t1; ++t, ++g) {
-            const int s = g % C::kKSt, d = g % C::kNS;
-            if (!waitb(&B->kfull[s], g / C::kKSt) || (g >= C::kNS && !waitb(&B->sempty[d], g / C::kNS - 1))) {
+            const int d = g % C::kNS;
+            if (!waitb(&B->kfull[s], lap) || (g >= C::kNS && !waitb(&B->sempty[d], g / C::kNS - 1))) {
               ok = false;
               break;
             }
@@ -667,9 +722,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc_commit(done);
             }
             __syncwarp();
+            if (++s == C::kKSt) {
+              s = 0;
+              ++lap;
+            }
           }
-          if (ok && el) tc_commit(bar_at(B->qk_done, n & 1));
-          __syncwarp();
         }
         if (ok && el) tc_commit(bar_at(B->q_empty, m & 1));
         __syncwarp();
@@ -723,28 +780,163 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (el) tc_commit(smem_u32(&B->fin[warp & 1]));
     __syncwarp();
     mbar_wait(smem_u32(&B->fin[warp & 1]), 0);   // not cut short by an abort: the work is in flight
-  } else {
-    // ================================================================ softmax warps ====
-    const int sg = (warp - kSoftWarp0) >> 2;        // warpgroup: rows [sg NH, sg NH + NH)
+  } else if (warp < kPWarp0) {
+    // =================================================================== first pass ====
     const int q4 = warp & 3;                        // tensor-memory lane quarter
-    const int lrow = q4 * 32 + lane;                // tile position (S) or d (O) of this thread
+    const int lrow = q4 * 32 + lane;                // tile position of this thread
+    const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16);
+    uint32_t wg_phase = 0;
+    // lane j keeps the running reference of row j (half j / NR); the four warps hold the same values
+    float mrun = 0.f;
+    const int jl = lane < 2 * NR ? lane : 2 * NR - 1, jc = jl / NR * NH + jl % NR;   // row, its column
+    bool ok = true;
+    int n = 0, g = 0, s = 0, lap = 0;   // chunks, tiles; position in the K ring
+#pragma unroll 1
+    for (int m = 0; ok && !aborted(abort_flag); ++m) {
+      Span x;
+      if (!ring_span(m, x)) break;
+      const int L = x.L, Lc = x.L + T;
+      const int rows = min(p.Rg, R - x.g0);
+      float* scores = CAP && p.scores ? p.scores + (((size_t)x.r * Hkv + x.kvh) * R + x.g0) * (size_t)p.cap : nullptr;
+      const float* rsm = rs + (m & 7) * NP;
+#pragma unroll 1
+      for (int t0 = x.t0; t0 < x.t1; t0 += C::kMT, ++n) {
+        const int nt = min(C::kMT, x.t1 - t0);
+        // the chunk's page scales; its logits' buffer (with the first tile: the span's row factors)
+        if (!waitb(&B->sc_full[n & (kScaleBufs - 1)], n / kScaleBufs) ||
+            (n >= 2 && !waitb(&B->x_empty[n & 1], (n - 2) >> 1))) {
+          ok = false;
+          break;
+        }
+        const float* ksc = scs + (n & (kScaleBufs - 1)) * kScaleFloats + (lrow >> 4);   // + 8 per tile
+        const float* lvc = ksc + 128;
+        float2 mrow[2 * RP];
+#pragma unroll
+        for (int j = 0; j < 2 * RP; ++j) mrow[j] = make_float2(-INFINITY, -INFINITY);
+#pragma unroll 1
+        for (int u = 0; u < nt; ++u, ++g) {
+          const int d = g % C::kNS;
+          if (!waitb(&B->qkd[s], lap)) {
+            ok = false;
+            break;
+          }
+          if (++s == C::kKSt) {
+            s = 0;
+            ++lap;
+          }
+          tc_fence_after();
+          float v[2][NP];   // per half of the rows: NH of qh, NH of ql
+          tmem_ld<NP>(tl + C::kSCol0 + d * 2 * NP, v[0]);
+          tmem_ld<NP>(tl + C::kSCol0 + d * 2 * NP + NP, v[1]);
+          tmem_wait_ld();
+          tmem_tie(v[0]);
+          tmem_tie(v[1]);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&B->sempty[d]));
+          const int p0 = (t0 + u) * kPos, pos = p0 + lrow;
+          const float ks = ksc[u * 8], lv = lvc[u * 8];
+          const float2 ks2 = make_float2(ks, ks), lv2 = make_float2(lv, lv);
+          // masked: the tile holds positions that some row does not see (compiled apart without capture,
+          // so that the other tiles' code is straight; with capture one copy is faster)
+          auto take = [&](auto m_) {
+            const bool masked = m_;
+            // the first row that sees the position: pos - L <= its block row
+            const int r0 = pos < L ? 0 : (pos < Lc ? (pos - L) * G - x.g0 : kPos);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float2 y[RP];
+#pragma unroll
+              for (int j = 0; j < RP; ++j)
+                y[j] = mul2(mul2(add2(make_float2(v[h][2 * j], v[h][2 * j + 1]),
+                                      make_float2(v[h][NH + 2 * j], v[h][NH + 2 * j + 1])), ks2),
+                            *reinterpret_cast<const float2*>(rsm + h * NH + 2 * j));
+              if (scores && pos < L) {
+                // a warp's 32 lanes write 32 consecutive positions of a row, one whole 128-byte line
+                float* srow = scores + (size_t)(h * NR) * p.cap + pos;
+#pragma unroll
+                for (int j = 0; j < RP; ++j) {
+                  if (h * NR + 2 * j < rows) *srow = y[j].x * kLn2;
+                  srow += p.cap;
+                  if (h * NR + 2 * j + 1 < rows) *srow = y[j].y * kLn2;
+                  srow += p.cap;
+                }
+              }
+              if (masked) {
+#pragma unroll
+                for (int j = 0; j < RP; ++j) {
+                  if (h * NR + 2 * j < r0) y[j].x = -INFINITY;
+                  if (h * NR + 2 * j + 1 < r0) y[j].y = -INFINITY;
+                }
+              }
+              float xo[NH];
+#pragma unroll
+              for (int j = 0; j < NH; ++j) xo[j] = j < NR ? ((j & 1) ? y[j / 2].y : y[j / 2].x) : 0.f;
+              tmem_st(tl + C::kXCol0 + ((n & 1) * C::kMT + u) * NP + h * NH, xo);
+#pragma unroll
+              for (int j = 0; j < RP; ++j) {
+                const float2 z = add2(y[j], lv2);
+                mrow[h * RP + j].x = fmaxf(mrow[h * RP + j].x, z.x);
+                mrow[h * RP + j].y = fmaxf(mrow[h * RP + j].y, z.y);
+              }
+            }
+          };
+          if constexpr (CAP) take(p0 + kPos > L);
+          else if (__builtin_expect(p0 + kPos > L, 0)) take(std::true_type{});
+          else take(std::false_type{});
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        if (!ok) break;
+        {
+          float mx[2 * NR];
+#pragma unroll
+          for (int j = 0; j < 2 * NR; ++j) mx[j] = (j & 1) ? mrow[j / 2].y : mrow[j / 2].x;
+          const float r = ColReduce<2 * NR>::run(mx, lane, -INFINITY, [](float a, float b) { return fmaxf(a, b); });
+          const int c = ColReduce<2 * NR>::col_of(lane);
+          if (c < 2 * NR) redM[((n & 1) * 4 + q4) * NP + c] = r;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&B->wg[2]));
+        if (!waitb(&B->wg[2], wg_phase)) {
+          ok = false;
+          break;
+        }
+        wg_phase ^= 1u;
+        const float* m4 = redM + (n & 1) * 4 * NP + jl;
+        const float mc = fmaxf(fmaxf(m4[0], m4[NP]), fmaxf(m4[2 * NP], m4[3 * NP])) - 8.f;
+        const bool first = t0 == x.t0;
+        const float mn = first ? mc : fmaxf(mrun, mc);
+        if (q4 == 0 && lane < 2 * NR) {
+          float* rf = refs + (n & 3) * 3 * NP + jc;
+          rf[0] = mn == -INFINITY ? 0.f : -mn;   // nothing seen yet: 2^-inf = 0
+          rf[NP] = first || mrun == -INFINITY ? 0.f : exp2f(mrun - mn);
+          rf[2 * NP] = mn;
+        }
+        mrun = mn;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&B->x_full[n & 1]));
+      }
+    }
+  } else {
+    // ================================================================== second pass ====
+    const int sg = (warp - kPWarp0) >> 2;           // warpgroup: rows [sg NR, sg NR + NR)
+    const int q4 = warp & 3;
+    const int lrow = q4 * 32 + lane;                // tile position (x) or d (O) of this thread
     const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16);
     // 16-byte chunk XOR of this position's P^T row (32-, 64-byte swizzle)
     const int swz_row = NP == 16 ? ((lrow >> 2) & 1) : ((lrow >> 1) & 3);
     uint32_t wg_phase = 0;
-    auto wg_sync = [&]() -> bool {   // bounded, unlike bar.sync
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&B->wg[sg]));
-      const bool r = wait_warp(smem_u32(&B->wg[sg]), wg_phase, abort_flag, p.err, p.wait_limit);
-      wg_phase ^= 1u;
-      return r;
-    };
-    float* nmw = own + (sg * 4 + q4) * 3 * NH;   // this warp's copies of the group's rows: -reference,
-    float* faw = nmw + NH;                       //   factor of what came before (by chunk parity)
     float orun[NR], lsum[NR];   // O of the span (this thread's d) and row sums, relative to the reference
     // Chunk n's O joins the span; with its last chunk the span's record (or, when the span is the
-    // whole context, the output) is written. mrec: the span's reference of row `lane`.
-    auto epilogue = [&](int n, const Span& x, bool first, bool last, int parity, float ov, float mrec) -> bool {
+    // whole context, the output) is written.
+    auto epilogue = [&](int n, int m, bool first, bool last, float ov) -> bool {
+      if (last) {   // the sums of the group's warps are there
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&B->wg[sg]));
+        if (!waitb(&B->wg[sg], wg_phase)) return false;
+        wg_phase ^= 1u;
+      }
       if (!waitb(&B->o_full[n & 1], n >> 1)) return false;
       tc_fence_after();
       float o[NP];
@@ -753,30 +945,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&B->o_empty[n & 1]));
-      const float* fan = faw + (n & 1) * NH;
+      const float* rf = refs + (n & 3) * 3 * NP + sg * NH;
 #pragma unroll
       for (int j = 0; j < NR; ++j) {
         const float v = fmaf(o[NH + j], 0.03125f, o[j]) * ov;
-        orun[j] = first ? v : fmaf(orun[j], fan[j], v);
+        orun[j] = first ? v : fmaf(orun[j], rf[NP + j], v);
       }
       if (!last) return true;
+      Span x;
+      read_span(m, x);
       const int rows = min(NR, min(p.Rg, R - x.g0) - sg * NR), row0 = x.g0 + sg * NR;
-      const float* rl4 = redL + parity * 8 * NH + sg * 4 * NH;   // sums of the group's warps
+      const float* rl4 = redL + (m & 1) * 8 * NH + sg * 4 * NH;   // sums of the group's warps
       if (x.nsp == 1) {
-        if (lrow < D) {
+#pragma unroll 1
+        for (int j = 0; j < rows; ++j) {   // (a loop: its code would otherwise be a quarter of the kernel)
+          float o = 0.f;
 #pragma unroll
-          for (int j = 0; j < NR; ++j) {
-            if (j < rows) {
-              const float l = (rl4[j] + rl4[NH + j]) + (rl4[2 * NH + j] + rl4[3 * NH + j]);
-              const int t = (row0 + j) / G, gq = row0 + j - t * G;
-              p.out[(((size_t)x.r * T + t) * p.Hq + x.kvh * G + gq) * D + lrow] = __float2bfloat16_rn(orun[j] / l);
-            }
-          }
-        }
-        if (q4 == 0 && lane < rows) {
-          const float l = (rl4[lane] + rl4[NH + lane]) + (rl4[2 * NH + lane] + rl4[3 * NH + lane]);
-          const int row = row0 + lane, t = row / G, gq = row - t * G;
-          p.lse[((size_t)x.r * T + t) * p.Hq + x.kvh * G + gq] = (mrec + log2f(l)) * kLn2;
+          for (int i = 0; i < NR; ++i)
+            if (i == j) o = orun[i];
+          const float l = (rl4[j] + rl4[NH + j]) + (rl4[2 * NH + j] + rl4[3 * NH + j]);
+          const int t = (row0 + j) / G, gq = row0 + j - t * G;
+          const size_t orow = ((size_t)x.r * T + t) * p.Hq + x.kvh * G + gq;
+          if (lrow < D) p.out[orow * D + lrow] = __float2bfloat16_rn(o / l);
+          if (lrow == 0) p.lse[orow] = (rf[2 * NP + j] + log2f(l)) * kLn2;
         }
         return true;
       }
@@ -787,148 +978,58 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (j < rows) rec[2 * p.Rp + (size_t)(sg * NR + j) * D + lrow] = orun[j];
       }
       if (q4 == 0 && lane < rows) {
-        rec[sg * NR + lane] = mrec;
+        rec[sg * NR + lane] = rf[2 * NP + lane];
         rec[p.Rp + sg * NR + lane] = (rl4[lane] + rl4[NH + lane]) + (rl4[2 * NH + lane] + rl4[3 * NH + lane]);
       }
       return true;
     };
 
     bool ok = true;
-    int n = 0, gs = 0;          // chunk and tile counters
-    // Lane j of every warp of the group keeps row j's reference; the four warps hold the same
-    // values, so the exchange of the chunk maxima is the one barrier of a chunk.
-    float mrun = 0.f, mrec = 0.f, ovp = 0.f;
-    const int jl = lane < NR ? lane : NR - 1;
-    Span xp{};
+    int n = 0, gs = 0;          // chunks, tiles
+    float ovp = 0.f;            // of the chunk before: unit of V scales, span, place in it
+    int mp = 0;
     bool pfirst = false, plast = false;
-    int mpar = 0;               // parity of the span before the current one
+#pragma unroll 1
     for (int m = 0; ok && !aborted(abort_flag); ++m) {
       Span x;
       if (!ring_span(m, x)) break;
-      const int L = x.L, Lc = x.L + T;
-      const int row0 = x.g0 + sg * NR, rows = min(p.Rg, R - x.g0) - sg * NR;
-      float* scores = p.scores ? p.scores + (((size_t)x.r * Hkv + x.kvh) * R + row0) * (size_t)p.cap : nullptr;
-      const float* rsm = rs + (m & 3) * NP + sg * NH;
-      for (int t0 = x.t0; t0 < x.t1 && ok; t0 += C::kMT, ++n) {
-        const int t1 = min(t0 + C::kMT, x.t1), nt = t1 - t0;
-        const bool first = t0 == x.t0, last = t1 == x.t1;
-        // the chunk's page scales, and with its first tile the span's row factors
-        if (!waitb(&B->sc_full[n & (kScaleBufs - 1)], n / kScaleBufs) ||
-            !waitb(&B->qkd[gs % C::kKSt], gs / C::kKSt)) {
+#pragma unroll 1
+      for (int t0 = x.t0; t0 < x.t1; t0 += C::kMT, ++n) {
+        const int nt = min(C::kMT, x.t1 - t0);
+        const bool first = t0 == x.t0, last = t0 + nt == x.t1;
+        if (!waitb(&B->x_full[n & 1], n >> 1)) {
           ok = false;
           break;
         }
-        const float* ksc = scs + (n & (kScaleBufs - 1)) * kScaleFloats + (lrow >> 4);   // + 8 per tile
-        const float* vsc = ksc + 64;
-        const float* lvc = ksc + 128;
-
-        // pass 1: logits x (log2 units, -inf where a row does not see the position) to tensor
-        // memory, committed ones out; per row the maximum of x + log2(vs / vref)
-        float2 mrow[RP], rs2[RP];
-#pragma unroll
-        for (int j = 0; j < RP; ++j) {
-          mrow[j] = make_float2(-INFINITY, -INFINITY);
-          rs2[j] = make_float2(rsm[2 * j], rsm[2 * j + 1]);
-        }
-        for (int u = 0; u < nt; ++u) {
-          const int d = (gs + u) % C::kNS;
-          if (u > 0 && !waitb(&B->qkd[(gs + u) % C::kKSt], (gs + u) / C::kKSt)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          float v[NP];
-          tmem_ld<NP>(tl + C::kSCol0 + d * 2 * NP + sg * NP, v);
-          tmem_ready(v);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&B->sempty[d]));
-          const int p0 = (t0 + u) * kPos, pos = p0 + lrow;
-          const float ks = ksc[u * 8], lv = lvc[u * 8];
-          const float2 ks2 = make_float2(ks, ks), lv2 = make_float2(lv, lv);
-          float2 y[RP];
-#pragma unroll
-          for (int j = 0; j < RP; ++j)
-            y[j] = mul2(mul2(add2(make_float2(v[2 * j], v[2 * j + 1]), make_float2(v[NH + 2 * j], v[NH + 2 * j + 1])), ks2),
-                        rs2[j]);
-          if (scores && pos < L) {
-            // a warp's 32 lanes write 32 consecutive positions of a row, one whole 128-byte line
-#pragma unroll
-            for (int j = 0; j < RP; ++j) {
-              if (2 * j < rows) scores[(size_t)(2 * j) * p.cap + pos] = y[j].x * kLn2;
-              if (2 * j + 1 < rows) scores[(size_t)(2 * j + 1) * p.cap + pos] = y[j].y * kLn2;
-            }
-          }
-          if (p0 + kPos > L) {
-            // the first row (of this warpgroup's) that sees the position: pos - L <= its block row
-            const int r0 = pos < L ? 0 : (pos < Lc ? (pos - L) * G - row0 : kPos);
-#pragma unroll
-            for (int j = 0; j < RP; ++j) {
-              if (2 * j < r0) y[j].x = -INFINITY;
-              if (2 * j + 1 < r0) y[j].y = -INFINITY;
-            }
-          }
-          float xs[NH];
-#pragma unroll
-          for (int j = 0; j < NH; ++j) xs[j] = j < NR ? ((j & 1) ? y[j / 2].y : y[j / 2].x) : 0.f;
-          tmem_st(tl + C::kXCol0 + u * NP + sg * NH, xs);
-#pragma unroll
-          for (int j = 0; j < RP; ++j) {
-            const float2 z = add2(y[j], lv2);
-            mrow[j].x = fmaxf(mrow[j].x, z.x);
-            mrow[j].y = fmaxf(mrow[j].y, z.y);
-          }
-        }
-        tmem_wait_st();
-        if (!ok) break;
-        {
-          float mx[NR];
-#pragma unroll
-          for (int j = 0; j < NR; ++j) mx[j] = (j & 1) ? mrow[j / 2].y : mrow[j / 2].x;
-          const float r = ColReduce<NR>::run(mx, lane, -INFINITY, [](float a, float b) { return fmaxf(a, b); });
-          const int c = ColReduce<NR>::col_of(lane);
-          if (c < NR) redM[((n & 1) * 8 + sg * 4 + q4) * NH + c] = r;
-        }
-        if (!wg_sync()) {
-          ok = false;
-          break;
-        }
-        const float vref = scs[(n & (kScaleBufs - 1)) * kScaleFloats + 192];
-        {
-          const float* m4 = redM + (n & 1) * 8 * NH + sg * 4 * NH + jl;
-          const float mc = fmaxf(fmaxf(m4[0], m4[NH]), fmaxf(m4[2 * NH], m4[3 * NH])) - 8.f;
-          const float mn = first ? mc : fmaxf(mrun, mc);
-          const float a = first || mrun == -INFINITY ? 0.f : exp2f(mrun - mn);
-          mrun = mn;
-          if (lane < NR) {
-            nmw[lane] = mn == -INFINITY ? 0.f : -mn;   // nothing seen yet: 2^-inf = 0
-            faw[(n & 1) * NH + lane] = a;
-          }
-        }
-        __syncwarp();
+        tc_fence_after();
+        const float* vsc = scs + (n & (kScaleBufs - 1)) * kScaleFloats + 64 + (lrow >> 4);   // + 8 per tile
+        const float* rf = refs + (n & 3) * 3 * NP + sg * NH;
+        const uint32_t xb = tl + C::kXCol0 + (n & 1) * C::kMT * NP + sg * NH;
+        float v[NH];
+        tmem_ld<NH>(xb, v);
         float2 nm[RP];
 #pragma unroll
-        for (int j = 0; j < RP; ++j) nm[j] = make_float2(nmw[2 * j], nmw[2 * j + 1]);
-        const float* fan = faw + (n & 1) * NH;
-#pragma unroll
-        for (int j = 0; j < NR; ++j) lsum[j] = first ? 0.f : lsum[j] * fan[j];
-
-        // pass 2: 2^(x - m), its sum in fp32, times vs / vref in two e4m3 parts to P^T. The next
-        // tile's logits are on their way while this one is worked on, and a tile's P^T is handed
-        // over once the next one is ready to be stored (its stores have drained by then).
-        float v[NH];
-        tmem_ld<NH>(tl + C::kXCol0 + sg * NH, v);
+        for (int j = 0; j < RP; ++j) {
+          nm[j] = *reinterpret_cast<const float2*>(rf + 2 * j);
+          const float2 f = *reinterpret_cast<const float2*>(rf + NP + 2 * j);
+          lsum[2 * j] = first ? 0.f : lsum[2 * j] * f.x;
+          lsum[2 * j + 1] = first ? 0.f : lsum[2 * j + 1] * f.y;
+        }
+        // 2^(x - m), its sum in fp32, times vs / vref in two e4m3 parts to P^T. The next tile's logits
+        // are on their way while this one is worked on, and a tile's P^T is handed over once the
+        // next one is ready to be stored (its stores have drained by then).
         auto publish = [&](int slot) {
           fence_proxy_async();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&B->pfull[slot]));
         };
-        for (int u = 0; u < nt; ++u) {
+#pragma unroll 1
+        for (int u = 0; u < nt; ++u, ++gs) {
           tmem_ready(v);
           float2 e[RP];
 #pragma unroll
           for (int j = 0; j < RP; ++j) e[j] = add2(make_float2(v[2 * j], v[2 * j + 1]), nm[j]);
-          if (u + 1 < nt) tmem_ld<NH>(tl + C::kXCol0 + (u + 1) * NP + sg * NH, v);
+          if (u + 1 < nt) tmem_ld<NH>(xb + (u + 1) * NP, v);
           const float vw = vsc[u * 8];
           const float2 vw2 = make_float2(vw, vw);
           uint32_t all[NP / 4];
@@ -947,9 +1048,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             hw = (j & 1) ? __byte_perm(hw, h, 0x5410) : h;
             lw = (j & 1) ? __byte_perm(lw, l, 0x5410) : l;
           }
-          const int gp = gs + u, slot = gp % C::kPT;
-          if (u > 0) publish((gp - 1) % C::kPT);
-          if (gp >= C::kPT && !waitb(&B->pvd[slot], gp / C::kPT - 1)) {
+          const int slot = gs % C::kPT;
+          if (u > 0) publish((gs - 1) % C::kPT);
+          if (gs >= C::kPT && !waitb(&B->pvd[slot], gs / C::kPT - 1)) {
             ok = false;
             break;
           }
@@ -963,28 +1064,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_ld();   // nothing in flight when the tensor memory goes away
           break;
         }
-        publish((gs + nt - 1) % C::kPT);
-        if (lane == 0) mbar_arrive(smem_u32(&B->sm_done[n & 1]));
-        gs += nt;
-        // the previous chunk's O (its PV has had this chunk's passes to finish)
-        if (n > 0 && !epilogue(n - 1, xp, pfirst, plast, mpar, ovp, mrec)) {
+        const float vref = scs[(n & (kScaleBufs - 1)) * kScaleFloats + 192];
+        tc_fence_before();
+        publish((gs - 1) % C::kPT);
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&B->x_empty[n & 1]));
+          mbar_arrive(smem_u32(&B->sm_done[n & (kScaleBufs - 1)]));
+        }
+        // the previous chunk's O (its PV has had this chunk's pass to finish)
+        if (n > 0 && !epilogue(n - 1, mp, pfirst, plast, ovp)) {
           ok = false;
           break;
         }
         if (last) {
           const float r = ColReduce<NR>::run(lsum, lane, 0.f, [](float a, float b) { return a + b; });
           const int c = ColReduce<NR>::col_of(lane);
-          if (c < NR) redL[((m & 1) * 8 + sg * 4 + q4) * NH + c] = r;   // read behind the next barrier
+          if (c < NR) redL[((m & 1) * 8 + sg * 4 + q4) * NH + c] = r;   // read behind the epilogue's barrier
         }
-        xp = x;
+        mp = m;
         pfirst = first;
         plast = last;
-        mpar = m & 1;
         ovp = vref;
-        mrec = mrun;
       }
     }
-    if (ok && n > 0 && !aborted(abort_flag) && wg_sync()) epilogue(n - 1, xp, pfirst, plast, mpar, ovp, mrec);
+    if (ok && n > 0 && !aborted(abort_flag)) epilogue(n - 1, mp, pfirst, plast, ovp);
   }
 
   tc_fence_before();
@@ -1071,16 +1174,24 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kv8_kernel(const Verif
 
 }  // namespace kv8
 
-template <int RP, int D>
-static int launch_kv8_t(const CUtensorMap& k1, const CUtensorMap& v1, const CUtensorMap& k8,
+template <int RP, int D, bool CAP>
+static int launch_kv8_c(const CUtensorMap& k1, const CUtensorMap& v1, const CUtensorMap& k8,
                         const CUtensorMap& v8, const VerifyKv8Params& p, int batch, int num_sms,
                         cudaStream_t stream) {
   using C = kv8::Cfg<RP>;
   static std::atomic<uint64_t> attr_done{0};
-  if (cuda_status(ensure_smem_attr(kv8::verify_kv8_kernel<RP, D>, C::kSmem, attr_done), "cudaFuncSetAttribute") != S3R_OK)
+  if (cuda_status(ensure_smem_attr(kv8::verify_kv8_kernel<RP, D, CAP>, C::kSmem, attr_done), "cudaFuncSetAttribute") != S3R_OK)
     return S3R_ERR_CUDA;
-  launch_pdl(kv8::verify_kv8_kernel<RP, D>, num_sms, kv8::kThreads, C::kSmem, stream, k1, v1, k8, v8, p, batch);
+  launch_pdl(kv8::verify_kv8_kernel<RP, D, CAP>, num_sms, kv8::kThreads, C::kSmem, stream, k1, v1, k8, v8, p, batch);
   return cuda_status(cudaGetLastError(), "s3r_verify_attn_kv8");
+}
+
+template <int RP, int D>
+static int launch_kv8_t(const CUtensorMap& k1, const CUtensorMap& v1, const CUtensorMap& k8,
+                        const CUtensorMap& v8, const VerifyKv8Params& p, int batch, int num_sms,
+                        cudaStream_t stream) {
+  return p.scores ? launch_kv8_c<RP, D, true>(k1, v1, k8, v8, p, batch, num_sms, stream)
+                  : launch_kv8_c<RP, D, false>(k1, v1, k8, v8, p, batch, num_sms, stream);
 }
 
 template <int D>
@@ -1088,16 +1199,13 @@ static int launch_kv8_d(const CUtensorMap& k1, const CUtensorMap& v1, const CUte
                         const CUtensorMap& v8, const VerifyKv8Params& p, int batch, int num_sms,
                         cudaStream_t stream) {
   int st;
-  switch ((p.Rg + 3) / 4) {   // pairs of rows per warpgroup
-    case 1: st = launch_kv8_t<1, D>(k1, v1, k8, v8, p, batch, num_sms, stream); break;
-    case 2: st = launch_kv8_t<2, D>(k1, v1, k8, v8, p, batch, num_sms, stream); break;
-    case 3: st = launch_kv8_t<3, D>(k1, v1, k8, v8, p, batch, num_sms, stream); break;
-    case 4: st = launch_kv8_t<4, D>(k1, v1, k8, v8, p, batch, num_sms, stream); break;
-    case 5: st = launch_kv8_t<5, D>(k1, v1, k8, v8, p, batch, num_sms, stream); break;
-    case 6: st = launch_kv8_t<6, D>(k1, v1, k8, v8, p, batch, num_sms, stream); break;
-    case 7: st = launch_kv8_t<7, D>(k1, v1, k8, v8, p, batch, num_sms, stream); break;
-    default: st = launch_kv8_t<8, D>(k1, v1, k8, v8, p, batch, num_sms, stream); break;
-  }
+  const int rp = (p.Rg + 3) / 4;   // pairs of rows per warpgroup, up to the next instance
+  if (rp <= 1) st = launch_kv8_t<1, D>(k1, v1, k8, v8, p, batch, num_sms, stream);
+  else if (rp <= 2) st = launch_kv8_t<2, D>(k1, v1, k8, v8, p, batch, num_sms, stream);
+  else if (rp <= 4) st = launch_kv8_t<4, D>(k1, v1, k8, v8, p, batch, num_sms, stream);
+  else if (rp <= 5) st = launch_kv8_t<5, D>(k1, v1, k8, v8, p, batch, num_sms, stream);
+  else if (rp <= 7) st = launch_kv8_t<7, D>(k1, v1, k8, v8, p, batch, num_sms, stream);
+  else st = launch_kv8_t<8, D>(k1, v1, k8, v8, p, batch, num_sms, stream);
   if (st != S3R_OK) return st;
   dim3 grid((p.R + kv8::kMergeWarps - 1) / kv8::kMergeWarps, p.Hkv, batch);
   launch_pdl(kv8::merge_kv8_kernel<D>, grid, 32 * kv8::kMergeWarps, 0, stream, p, batch);
