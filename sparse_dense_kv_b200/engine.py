@@ -69,12 +69,48 @@ class RoundBuffers:
         self.q_norm = self._q_norm[: NR * k * 2].view(NR, k, 2)
 
 
+class PagePool:
+    """The pages of a pool that no request holds, as a stack on the GPU, and how many leading
+    entries of its page-table row each request holds: `grow` and `release` are one launch each on
+    the current stream and can be captured, so tables follow the lengths without the host.
+    Pages [0, num_pages) start free; the page table's entries are the pool's to write."""
+
+    def __init__(self, num_pages, page_table):
+        dev, nr = page_table.device, page_table.shape[0]
+        self.page_table = page_table
+        self.free_pages = torch.arange(num_pages - 1, -1, -1, dtype=torch.int32, device=dev)   # page 0 on top
+        self.free_count = torch.tensor([num_pages], dtype=torch.int32, device=dev)
+        self.held = torch.zeros((nr,), dtype=torch.int32, device=dev)
+        self.granted = torch.zeros((nr,), dtype=torch.int32, device=dev)
+        self.ws = L.new_workspace(L.s3r_pages_workspace_size(nr), dev)
+
+    def grow(self, batch, T, n_new=None, slot_map=None):
+        """Room for T (or n_new[r] <= T) tokens behind each request's committed length; granted[r]
+        says which requests have it (the stack may run out; see s3r_alloc_pages)."""
+        L.s3r_alloc_pages(batch, T, self.held, self.free_pages, self.free_count, self.held, self.free_count,
+                          self.granted, self.ws, n_new=n_new, slot_map=slot_map)
+
+    def release(self, batch, keep_len=None):
+        """Pages past ceil(keep_len[r] / 16) (None: all) of the batch's requests go back."""
+        L.s3r_release_pages(batch, self.held, self.free_pages, self.free_count, self.held, self.free_count, self.ws,
+                            keep_len=keep_len)
+
+    def check_errors(self) -> int:
+        """Synchronise and return (and clear) the device error bitmask of the page calls."""
+        return L.s3r_get_error(self.ws)
+
+
 class S3REngine:
-    """S3R rounds for a batch of requests over one paged KV cache on one GPU."""
+    """S3R rounds for a batch of requests over one paged KV cache on one GPU.
+
+    With k_scale and v_scale (fp32 [num_pages][num_kv_heads]) the pools are an 8-bit cache
+    (torch.float8_e4m3fn or uint8 codes): every row enters by s3r_kv8_append and the attention
+    calls are the kv8 ones; selection, sampling and commit are the same. With pages (a PagePool
+    over page_table) every prefill and round first grows the page tables by the rows it writes."""
 
     def __init__(self, k_pool, v_pool, page_table, seq_lens, num_q_heads, *, k, budget_bp,
                  window, vocab, seed, sel_stride=None, greedy=False, page_select=False, k_max=None,
-                 overlap_scores=True):
+                 overlap_scores=True, k_scale=None, v_scale=None, pages=None):
         k_max = k if k_max is None else k_max
         if not (1 <= k <= k_max <= L.MAX_K):
             raise ValueError("need 1 <= k <= k_max <= 8")
@@ -84,7 +120,16 @@ class S3REngine:
         self.k_pool, self.v_pool = k_pool, v_pool
         self.page_table = page_table
         self.seq_lens = seq_lens
-        self.cache = L.make_cache(k_pool, v_pool, num_q_heads)
+        self.cache8 = None     # descriptor of an 8-bit cache
+        if (k_scale is None) != (v_scale is None):
+            raise ValueError("an 8-bit cache needs k_scale and v_scale")
+        if k_scale is not None:
+            self.cache8 = L.make_kv8_cache(k_pool, v_pool, k_scale, v_scale, num_q_heads)
+        if pages is not None and pages.page_table is not page_table:
+            raise ValueError("pages must be the PagePool of this page table")
+        self.pages = pages
+        # selection takes the pools' shape only: the same calls serve both caches
+        self.cache = self.cache8.pools if self.cache8 is not None else L.make_cache(k_pool, v_pool, num_q_heads)
         self.num_requests, self.max_pages = page_table.shape
         self.cap = self.max_pages * L.PAGE_SIZE
         # a page-granular set holds up to 15 positions more than the token budget
@@ -94,8 +139,8 @@ class S3REngine:
                                 self.cache.head_dim, self.cap, k_max, vocab, self.sel_stride,
                                 k_pool.device)
         self.buf.set_k(k)
-        nbytes = L.s3r_workspace_size(self.cache, self.num_requests, self.max_pages, k_max, vocab,
-                                      self.sel_stride)
+        size, cache = (L.s3r_workspace_size, self.cache) if self.cache8 is None else (L.s3r_kv8_workspace_size, self.cache8)
+        nbytes = size(cache, self.num_requests, self.max_pages, k_max, vocab, self.sel_stride)
         self.ws = L.new_workspace(nbytes, k_pool.device)
         self.batch = L.make_batch(seq_lens, page_table)
         # The next selection's position scores (s3r_position_scores) are computed on a second
@@ -123,8 +168,27 @@ class S3REngine:
     @property
     def launches_per_round(self) -> int:
         # select (scores + select), k x (draft, sample), verify (attention launches + the chunk
-        # merge, as counted at the last verify), spec (2 / 1 greedy), commit
-        return 2 + 2 * self.k + self._verify_launches + (1 if self.greedy else 2) + 1
+        # merge, as counted at the last verify), spec (2 / 1 greedy), commit; an 8-bit cache appends
+        # each draft's row (the verify's append is counted with it), a page pool grows once
+        return (2 + 2 * self.k + self._verify_launches + (1 if self.greedy else 2) + 1
+                + (self.k if self.cache8 is not None else 0) + (1 if self.pages is not None else 0))
+
+    def _verify_call(self, batch, k, q, k_rows, v_rows, out, lse, scores):
+        if self.cache8 is None:
+            L.s3r_verify_attn(self.cache, batch, k, q, k_rows, v_rows, out, lse, scores, self.ws)
+            return
+        L.s3r_kv8_append(self.cache8, batch, k_rows, v_rows, self.ws)
+        L.s3r_verify_attn_kv8(self.cache8, batch, k, q, out, lse, scores, self.ws)
+
+    def _draft_call(self, batch, step, q, k_rows, v_rows):
+        b = self.buf
+        if self.cache8 is None:
+            L.s3r_sparse_draft_attn(self.cache, batch, step, q, k_rows, v_rows, b.sel_idx, b.sel_count, b.draft_out,
+                                    b.draft_lse, self.ws)
+            return
+        L.s3r_kv8_append(self.cache8, batch, k_rows.unsqueeze(1), v_rows.unsqueeze(1), self.ws, first=step)
+        L.s3r_sparse_draft_attn_kv8(self.cache8, batch, step, q, b.sel_idx, b.sel_count, b.draft_out, b.draft_lse,
+                                    self.ws)
 
     def prefill(self, q_x, k_x, v_x):
         """One-row dense pass of each request's pending token at position L (the last step of
@@ -132,8 +196,11 @@ class S3REngine:
         q_x [NR][1][H_q][d], k_x / v_x [NR][1][H_kv][d]."""
         b = self.buf
         out = torch.empty_like(q_x)
-        L.s3r_verify_attn(self.cache, self.batch, 0, q_x, k_x, v_x, out, b.prefill_lse, b.scores,
-                          self.ws)
+        if self.pages is not None:
+            self.pages.grow(self.batch, 1)
+        NR, Hq, Hkv, _, cap = b.dims
+        scores = b._scores[: NR * Hq * cap].view(NR, Hkv, Hq // Hkv, cap)   # one block row's layout
+        self._verify_call(self.batch, 0, q_x, k_x, v_x, out, b.prefill_lse, scores)
         self.k_prev = 0
         return out
 
@@ -150,10 +217,7 @@ class S3REngine:
            b.sel_idx, b.sel_count, self.ws)
 
     def draft_attn(self, i, q_block, k_block, v_block):
-        b = self.buf
-        L.s3r_sparse_draft_attn(self.cache, self.batch, b.steps[i], q_block[:, i], k_block[:, i],
-                                v_block[:, i], b.sel_idx, b.sel_count, b.draft_out, b.draft_lse,
-                                self.ws)
+        self._draft_call(self.batch, self.buf.steps[i], q_block[:, i], k_block[:, i], v_block[:, i])
 
     def draft_sample(self, i, q_logits):
         if self.greedy:
@@ -173,8 +237,7 @@ class S3REngine:
     def verify(self, q_block, k_block, v_block):
         b = self.buf
         before = L.s3r_launch_count()
-        L.s3r_verify_attn(self.cache, self.batch, self.k, q_block, k_block, v_block, b.verify_out,
-                          b.lse, b.scores, self.ws)
+        self._verify_call(self.batch, self.k, q_block, k_block, v_block, b.verify_out, b.lse, b.scores)
         self._verify_launches = L.s3r_launch_count() - before
         self.k_prev = self.k
         self._scores_ready = False
@@ -217,6 +280,8 @@ class S3REngine:
         callbacks when given)."""
         if self.k_prev is None:
             raise RuntimeError("call prefill() before the first round")
+        if self.pages is not None:
+            self.pages.grow(self.batch, self.k + 1)
         self.select()
         for i in range(self.k):
             self.draft_step(i, q_block, k_block, v_block, q_logits, draft_logits_fn)
@@ -266,6 +331,8 @@ class MixedPhaseDriver:
         if self.phases.shape != (engine.num_requests,) or self.phases.min() < 0 or \
                 self.phases.max() > engine.k:
             raise ValueError("one phase in 0..k per request")
+        if engine.pages is not None:
+            raise ValueError("requests at different phases grow at different times: grow the PagePool by hand")
         dev = engine.k_pool.device
         self.step = torch.zeros((engine.num_requests,), dtype=torch.int32, device=dev)
         self._dev = dev
@@ -314,8 +381,7 @@ class MixedPhaseDriver:
         kc = k_block[ar, rows].contiguous()
         vc = v_block[ar, rows].contiguous()
         batch = self._batch(ids)
-        L.s3r_sparse_draft_attn(e.cache, batch, self.step, qc, kc, vc, b.sel_idx, b.sel_count,
-                                b.draft_out, b.draft_lse, e.ws)
+        e._draft_call(batch, self.step, qc, kc, vc)
         if e.greedy:
             L.s3r_draft_argmax(batch, self.step, e.k, q_logits, e.vocab, b.draft_tokens, e.ws)
         else:
@@ -357,8 +423,7 @@ class MixedPhaseDriver:
                 rec = (lambda n: ev[n].record()) if ev is not None else (lambda n: None)
                 rec("d0")
                 if it["n_draft"]:
-                    L.s3r_sparse_draft_attn(e.cache, it["d_batch"], it["step"], it["qc"], it["kc"], it["vc"],
-                                            b.sel_idx, b.sel_count, b.draft_out, b.draft_lse, e.ws)
+                    e._draft_call(it["d_batch"], it["step"], it["qc"], it["kc"], it["vc"])
                 rec("dm")
                 if it["n_draft"]:
                     if e.greedy:
@@ -370,8 +435,7 @@ class MixedPhaseDriver:
                 rec("v0")
                 if it["n_verify"]:
                     vb = it["v_batch"]
-                    L.s3r_verify_attn(e.cache, vb, k, q_block, k_block, v_block, b.verify_out, b.lse,
-                                      b.scores, e.ws)
+                    e._verify_call(vb, k, q_block, k_block, v_block, b.verify_out, b.lse, b.scores)
                     rec("v1")
 
                     def commit():
@@ -404,8 +468,7 @@ class MixedPhaseDriver:
             self._draft(d_ids, self.phases[d_ids], q_block, k_block, v_block, q_logits)
         if v_ids.size:
             batch = self._batch(v_ids)
-            L.s3r_verify_attn(e.cache, batch, e.k, q_block, k_block, v_block, b.verify_out, b.lse,
-                              b.scores, e.ws)
+            e._verify_call(batch, e.k, q_block, k_block, v_block, b.verify_out, b.lse, b.scores)
 
             def commit():
                 if e.greedy:
