@@ -22,9 +22,9 @@
 //
 // Work: grid (KV head, request, chunk of A_i), 4 warps; warp w takes the chunk's batches of 32
 // positions w, w + 4, .. and runs by itself (lane l resolves position l: index -> page -> row,
-// scales) with an online softmax; the selected index and the page of the next batch are fetched
-// one batch ahead. All K and V of a batch are in flight at once (8 KB per warp); 3 CTAs per SM
-// keep about 96 KB in flight. Warps merge in shared memory, chunks through the workspace in the
+// scales) with an online softmax. Its K registers take the next batch's rows as soon as S is
+// computed, its V registers as soon as O is, the indices run two batches ahead and the pages one, so
+// that 4 to 8 KB per warp are in flight all the time (12 warps per SM). Warps merge in shared memory, chunks through the workspace in the
 // last CTA of the (request, KV head). The chunk length follows from the launch: as many CTAs as
 // the SMs hold at once where there is enough to read, at least one batch per warp.
 #include "attention.cuh"
@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(128, kDraftKv8PerSm) draft_kv8_kernel(const Dr
   constexpr int RW = 8, KC = D / 64, VW = D / 32;   // 16-byte pieces of a K row per thread; words of a V row
   constexpr int MT = D / 16;                        // m-tiles of O^T
   __shared__ float redO[4 * RW * (D + 4)];
-  __shared__ float redM[4 * RW], redL[4 * RW], fw[4 * RW], Mrow[RW], Lrow[RW], wts[32 * RW];
+  __shared__ float redM[4 * RW], redL[4 * RW], fw[4 * RW], Mrow[RW], Lrow[RW];
   __shared__ int s_flag;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -152,18 +152,15 @@ __global__ void __launch_bounds__(128, kDraftKv8PerSm) draft_kv8_kernel(const Dr
   // running maxima of x and of z, sums relative to the former, O to the latter (- 10)
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f, z0 = kNoMax, z1 = kNoMax;
 
-  for (int b = start + warp * 32; b < end; b += 128) {
-    // row base (in 16 d-byte page blocks) of this lane's position; bad ones read nothing: zeros
-    const bool there = page >= 0;
+  uint4 kr[4][KC];       // rows of positions g, g + 8, g + 16, g + 24
+  uint32_t vr[8][VW];    // positions 2t, 2t+1, 2t+8, 2t+9 (+16)
+  float ks = 0.f, vs = 0.f, ksn = 0.f, vsn = 0.f;   // this lane's position's scales: the batch's, the next one's
+  // a position's row in the pools (d-byte rows); -1 for none (or a bad one): reads as zeros
+  auto row_of = [&](int page, int slot) -> int {
     if (page == -2) set_error(p.err, S3R_ERR_DEVICE_BOUNDS);
-    const int row = there ? (page * Hkv + kvh) * kPage + slot : -1;   // < 2^31 (checked at the call)
-    float ks = 0.f, vs = 0.f;
-    if (there) {
-      ks = __ldg(p.k_scale + (size_t)page * Hkv + kvh);
-      vs = __ldg(p.v_scale + (size_t)page * Hkv + kvh);
-    }
-    uint4 kr[4][KC];       // rows of positions g, g + 8, g + 16, g + 24
-    uint32_t vr[8][VW];    // positions 2t, 2t+1, 2t+8, 2t+9 (+16)
+    return page >= 0 ? (page * Hkv + kvh) * kPage + slot : -1;   // < 2^31 (checked at the call)
+  };
+  auto load_k = [&](int row) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int rw = __shfl_sync(kFull, row, g + 8 * i);
@@ -172,6 +169,8 @@ __global__ void __launch_bounds__(128, kDraftKv8PerSm) draft_kv8_kernel(const Dr
         kr[i][h] = rw >= 0 ? __ldg(reinterpret_cast<const uint4*>(p.k_pool + (size_t)rw * D + 64 * h + 16 * t))
                            : make_uint4(0, 0, 0, 0);
     }
+  };
+  auto load_v = [&](int row) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int pp = 16 * (i >> 2) + 8 * ((i >> 1) & 1) + 2 * t + (i & 1);
@@ -185,14 +184,28 @@ __global__ void __launch_bounds__(128, kDraftKv8PerSm) draft_kv8_kernel(const Dr
         vr[i][0] = x.x; vr[i][1] = x.y;
       }
     }
-    // the next batch's page, while this one's rows arrive
-    const int left = end - b;   // positions of this batch that count
+  };
+  auto load_scales = [&](int page, float& k, float& v) {
+    k = v = 0.f;
+    if (page >= 0) {
+      k = __ldg(p.k_scale + (size_t)page * Hkv + kvh);
+      v = __ldg(p.v_scale + (size_t)page * Hkv + kvh);
+    }
+  };
+  auto next_index = [&]() {   // the place a batch on, and its selected index
     a += 128;
     sidx = a < n ? __ldg(sel + a) : -1;
-    resolve(a, sidx, page, slot);
-    ks = good_scale(ks, p.err);
-    const float lv = log2f(good_scale(vs, p.err));   // -inf: nothing of this position in O
+  };
+  // first batch: its rows; the second's page
+  int row = row_of(page, slot);
+  load_scales(page, ks, vs);
+  load_k(row);
+  load_v(row);
+  next_index();
+  resolve(a, sidx, page, slot);
 
+  for (int b = start + warp * 32; b < end; b += 128) {
+    const int left = end - b;   // positions of this batch that count
     float s[2][4];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -208,6 +221,13 @@ __global__ void __launch_bounds__(128, kDraftKv8PerSm) draft_kv8_kernel(const Dr
                   qf[4 * h + q][0], qf[4 * h + q][1]);
       }
     }
+    // K's registers are free: the next batch's rows, while this one's weights are formed
+    row = row_of(page, slot);
+    load_scales(page, ksn, vsn);
+    load_k(row);
+    next_index();
+    ks = good_scale(ks, p.err);
+    const float lv = log2f(good_scale(vs, p.err));   // -inf: nothing of this position in O
     // logits in log2 units; positions g, g + 8 (s[0]), g + 16, g + 24 (s[1]), rows 2t, 2t + 1
     float mx0 = -INFINITY, mx1 = -INFINITY, mz0 = z0, mz1 = z1, lvp[2][2];
 #pragma unroll
@@ -271,6 +291,10 @@ __global__ void __launch_bounds__(128, kDraftKv8PerSm) draft_kv8_kernel(const Dr
           mma_f16(o[2 * wd + q], e4m3_lo_h2(xa), e4m3_hi_h2(xa), e4m3_lo_h2(ya), e4m3_hi_h2(ya), pf[u][0], pf[u][1]);
         }
       }
+    load_v(row);
+    ks = ksn;
+    vs = vsn;
+    resolve(a, sidx, page, slot);   // the batch after the next one's page
   }
 
   // warp results to shared memory: O in units of the row maximum, the V factor applied
@@ -311,7 +335,45 @@ __global__ void __launch_bounds__(128, kDraftKv8PerSm) draft_kv8_kernel(const Dr
     combine_few_records<D, RW>(recs, rec_floats, nch, G, out_row, lse_row, tid, blockDim.x);
     return;
   }
-  combine_records<D>(recs, rec_floats, nch, G, RW, wts, 32 * RW, out_row, lse_row, tid, blockDim.x);
+  // more records: a warp per row, their maxima and sums one per lane, their O four at a time
+  constexpr int V = D / 32;
+  for (int rr = warp; rr < G; rr += 4) {
+    float M = -INFINITY;
+    for (int q = lane; q < nch; q += 32) M = fmaxf(M, __ldcg(recs + q * rec_floats + rr));
+    M = warp_max(M);
+    float lsum = 0.f, acc[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.f;
+    for (int q0 = 0; q0 < nch; q0 += 32) {
+      float w = 0.f, l = 0.f;
+      if (q0 + lane < nch) {
+        const float ms = __ldcg(recs + (q0 + lane) * rec_floats + rr);
+        l = __ldcg(recs + (q0 + lane) * rec_floats + RW + rr);
+        w = ms == -INFINITY ? 0.f : exp2f(ms - M);
+      }
+      lsum = fmaf(w, l, lsum);
+      const int cnt = min(32, nch - q0);
+      const float* oq = recs + q0 * rec_floats + 2 * RW + (size_t)rr * D + lane * V;
+      for (int u = 0; u < cnt; u += 4) {
+        float x[4][V];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ld_vec<V>(oq + min(u + i, cnt - 1) * rec_floats, x[i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float wi = u + i < cnt ? __shfl_sync(kFull, w, (u + i) & 31) : __shfl_sync(kFull, 0.f, 0);
+#pragma unroll
+          for (int j = 0; j < V; ++j) acc[j] = fmaf(wi, x[i][j], acc[j]);
+        }
+      }
+    }
+#pragma unroll
+    for (int x = 16; x; x >>= 1) lsum += __shfl_xor_sync(kFull, lsum, x);
+    __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(out_row(rr) + lane * V);
+#pragma unroll
+    for (int i = 0; i < V; i += 2) dst[i / 2] = __floats2bfloat162_rn(acc[i] / lsum, acc[i + 1] / lsum);
+    float* lp = lse_row(rr);
+    if (lane == 0 && lp) *lp = (M + log2f(lsum)) * kLn2;
+  }
 }
 
 // Positions per CTA: the launch's (request, KV head) sets, each up to sel_stride positions, over
