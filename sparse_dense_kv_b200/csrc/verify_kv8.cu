@@ -70,7 +70,6 @@ using namespace tc;
 
 constexpr int kPos = 128;
 constexpr int kThreads = 512;
-constexpr int kXWarp0 = 4;                // first pass: 4 warps
 constexpr int kPWarp0 = 8;                // second pass: 8 warps
 constexpr int kTileBytes = kPos * 128;    // 16 KB: 128 positions x 128 bytes (d = 64: half zero)
 constexpr int kRing = 16;
