@@ -132,20 +132,41 @@ __global__ void __launch_bounds__(kPagesThreads) pages_kernel(const PagesParams 
     }
   }
   if (!RELEASE && p.slot_map) {
-    // slots of the segment, flattened over the CTA's requests
     const int t0 = blockIdx.x * kAllocSeg, seg = min(kAllocSeg, p.T - t0);
-    for (int k = tid; k < nb * seg; k += kPagesThreads) {
-      const int i = k / seg, t = t0 + k - i * seg;
-      const PageDemand& x = dem[i];
-      if (x.r < 0) continue;
-      int64_t slot = -1;
-      if (!x.bad && t < x.n) {
-        const int pos = x.L + t, pg = pos / kPage;
-        const int page = pg < x.held ? p.page_table[(size_t)x.r * p.max_pages + pg]
-                                     : p.free_pages[have - 1 - before_s[i] - (pg - x.held)];
-        slot = (int64_t)page * kPage + pos % kPage;
+    // the slot of a request's token t; -1 where it has none
+    auto slot_of = [&](const PageDemand& x, long long top, int t) -> int64_t {
+      if (x.bad || t >= x.n) return -1;
+      const uint32_t pos = (uint32_t)(x.L + t);
+      const int pg = (int)(pos / kPage);
+      const int page = pg < x.held ? p.page_table[(size_t)x.r * p.max_pages + pg] : p.free_pages[top - pg];
+      return (int64_t)page * kPage + pos % kPage;
+    };
+    if (p.T >= 2 * kPagesThreads) {
+      // long rows: two slots per store where the row's address allows it, four stores in flight
+      for (int i = 0; i < nb; ++i) {
+        const PageDemand x = dem[i];
+        if (x.r < 0) continue;
+        const long long top = have - 1 - before_s[i] + x.held;
+        int64_t* row = p.slot_map + (size_t)x.r * p.T + t0;
+        const int odd = (int)(((uintptr_t)row >> 3) & 1);
+        const int pairs = (seg - odd) / 2;
+        if (tid == 0 && odd) row[0] = slot_of(x, top, t0);
+        if (tid == 0 && odd + 2 * pairs < seg) row[seg - 1] = slot_of(x, top, t0 + seg - 1);
+        longlong2* out = reinterpret_cast<longlong2*>(row + odd);
+#pragma unroll 4
+        for (int k = tid; k < pairs; k += kPagesThreads) {
+          const int t = t0 + odd + 2 * k;
+          out[k] = make_longlong2(slot_of(x, top, t), slot_of(x, top, t + 1));
+        }
       }
-      p.slot_map[(size_t)x.r * p.T + t] = slot;
+    } else {
+      // short rows, flattened over the CTA's requests
+      for (int k = tid; k < nb * seg; k += kPagesThreads) {
+        const int i = k / seg, t = t0 + k - i * seg;
+        const PageDemand& x = dem[i];
+        if (x.r < 0) continue;
+        p.slot_map[(size_t)x.r * p.T + t] = slot_of(x, have - 1 - before_s[i] + x.held, t);
+      }
     }
   }
 
