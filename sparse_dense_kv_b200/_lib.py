@@ -318,8 +318,9 @@ def _call_device(*descs):
     """The device of the descriptors' tensors, which must be the current one (the stream and the
     launch are the current device's)."""
     device = descs[0]._device
-    if any(d._device != device for d in descs):
-        raise ValueError("cache and batch are on different devices")
+    for d in descs[1:]:
+        if d._device != device:
+            raise ValueError("cache and batch are on different devices")
     if device.index != torch.cuda.current_device():
         raise ValueError(f"the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
     return device
@@ -332,7 +333,10 @@ def _ws_arg(ws, device):
 
 
 def _batch_table(batch):
-    """(num_requests, page table) of a batch made with a page table."""
+    """(num_requests, page table) of a batch made with a page table; checked at its first call."""
+    known = getattr(batch, "_table", None)
+    if known is not None and known[0] == batch.num_requests:
+        return known
     seq_lens, pt, req_ids = batch._refs
     if pt is None:
         raise ValueError("the batch needs a page table")
@@ -340,11 +344,14 @@ def _batch_table(batch):
         raise ValueError(f"the page table has {pt.shape[0]} rows for {batch.num_requests} requests")
     if pt.device != seq_lens.device or (req_ids is not None and req_ids.device != seq_lens.device):
         raise ValueError("the batch's tensors are on different devices")
-    return batch.num_requests, pt
+    batch._table = (batch.num_requests, pt)
+    return batch._table
 
 
 def _stream_ptr(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+    if stream is None:   # the handle alone: a Stream object takes a microsecond
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def make_kv8_cache(k_pool: torch.Tensor, v_pool: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
