@@ -261,7 +261,9 @@ S3R_API int s3r_kv8_append(const s3r_kv8_cache* cache, const s3r_batch* batch, c
 
 /* Dense verify attention over an 8-bit cache: rows t = 0..k of request r at positions L+t,
  * row t of each query head attending positions 0..L+t of the cache (k = 0: one decode row).
- * q, out, lse, score_logits as for s3r_verify_attn; sums, maxima and logits in fp32. */
+ * q, out, lse, score_logits as for s3r_verify_attn; sums, maxima and logits in fp32. V scales
+ * above 2^48 (values of 10^17) are taken as 2^48 and set S3R_ERR_NONFINITE; a page whose V scale
+ * is below 2^-88 of another's of its request and KV head may count as zeros. */
 S3R_API int s3r_verify_attn_kv8(const s3r_kv8_cache* cache, const s3r_batch* batch, int32_t k,
                         const void* q, void* out, float* lse, float* score_logits, void* ws,
                         size_t ws_bytes, s3r_stream_t stream);

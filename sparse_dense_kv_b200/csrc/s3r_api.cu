@@ -632,7 +632,7 @@ int s3r_kv8_append(const s3r_kv8_cache* cache, const s3r_batch* batch, const int
                    size_t ws_bytes, s3r_stream_t stream) {
   S3R_TRY(check_kv8_cache(cache));
   S3R_TRY(check_batch(batch, true));
-  if (T < 0) return S3R_ERR_INVALID_ARG;
+  if (T < 0 || T >= (1 << 30)) return S3R_ERR_INVALID_ARG;
   if (!k_new || !v_new || !aligned16(k_new) || !aligned16(v_new) || (first && !aligned4(first)) ||
       (n_new && !aligned4(n_new)))
     return S3R_ERR_INVALID_ARG;

@@ -16,9 +16,9 @@
 //     split is exact down to 2^-10 of the row's largest element and off by at most 2^-18 of it
 //     below.
 //   p = 2^(x - m) vs / vref, the row's reference m (log2 units) such that the largest p so far is
-//     256: m = max(x + log2(vs / vref)) - 8 (vref: the largest V scale of the span's first chunk),
-//     so a weight keeps its precision next to what it contributes to the output, whatever the page
-//     scales are (up to 2^64 apart within a span). ph = e4m3(p),
+//     256: m = max(x + log2(vs / vref)) - 8 (vref: the largest V scale of the span's first chunk,
+//     at least 2^-40), so a weight keeps its precision next to what it contributes to the output,
+//     whatever the page scales are (down to 2^-88 of vref). ph = e4m3(p),
 //     pl = e4m3(32 (p - ph)): within 2^-9 of p (bf16's half step is 2^-9 of the next power of
 //     two), and within 2^-23 of the largest p below the normal range.
 // The two parts stand side by side along N in both products (2 NP columns): an MMA of M = 128,
@@ -26,7 +26,7 @@
 // what a tile's 12 MMAs (both parts into one S) were waiting for; with 8 the softmax is.
 // The scales enter in fp32: ks times the logit of its position (one tensor-memory lane = one
 // position = one page), vs / vref into p, vref into O. The row sums are those of 2^(x - m) in fp32;
-// m need not be the row's maximum (it is within 72 of it).
+// m need not be the row's maximum (it is within 96 of it).
 //
 // Organisation: one persistent CTA per SM. A work item is a span of consecutive tiles of 128
 // positions of one (request, KV head, row group); more than 32 rows are two groups of half the rows,
@@ -74,7 +74,11 @@ constexpr int kPWarp0 = 8;                // second pass: 8 warps
 constexpr int kTileBytes = kPos * 128;    // 16 KB: 128 positions x 128 bytes (d = 64: half zero)
 constexpr int kRing = 16;
 constexpr int kScaleBufs = 8;             // chunks whose page scales are held
-constexpr int kScaleFloats = 196;         // ks, vs / vref, log2 of that (>= -64) [64] each; vref; pad
+// V scales: vs / vref is at most 2^88, since vref >= 2^-40 and larger scales than 2^48 are refused,
+// and its logarithm counts as at least -88, so that the terms of a row sum lie between 2^-80 (a
+// logit at the reference's) and 2^96.
+constexpr float kMaxVScale = 0x1p48f, kMaxRatio = 88.f;
+constexpr int kScaleFloats = 196;         // ks, vs / vref, log2 of that (>= -kMaxRatio) [64] each; vref; pad
 constexpr int kMaxSt = 6;                 // ring stages
 constexpr int kBarBytes = 1792;           // barriers, flags, the ring of spans
 constexpr int kMaxBatch = 256;            // requests per launch (larger batches: several launches)
@@ -629,6 +633,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         vb = __ldg(p.v_scale + (size_t)idb * Hkv + y.kvh);
       }
     };
+    auto good_v_scale = [&](float v) -> float {
+      v = good_scale(v, p.err);
+      if (v > kMaxVScale) set_error(p.err, S3R_ERR_NONFINITE);
+      return fminf(v, kMaxVScale);
+    };
     if (more && !is_v) fetch_scales(x);
     while (more && !stop && !aborted(abort_flag)) {
       survey(x, t0, t1, ida, idb);
@@ -638,20 +647,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (stop) break;
       if (!is_v) {
         float* sc = scs + (n & (kScaleBufs - 1)) * kScaleFloats;
-        va = good_scale(va, p.err);
-        vb = good_scale(vb, p.err);
-        if (t0 == x.t0) {   // the span's unit of V scales: the largest of its first chunk
-          const float vmax = warp_max(fmaxf(va, vb));
-          vref = vmax >= 0x1p-120f ? vmax : 1.f;
-        }
-        const float inv = 1.f / vref;
-        const float ra = fminf(va * inv, 0x1p64f), rb = fminf(vb * inv, 0x1p64f);
+        va = good_v_scale(va);
+        vb = good_v_scale(vb);
+        // the span's unit of V scales: the largest of its first chunk, at least 2^-40
+        if (t0 == x.t0) vref = fmaxf(warp_max(fmaxf(va, vb)), 0x1p-40f);
+        const float inv = 1.f / vref, ra = va * inv, rb = vb * inv;
         sc[lane] = good_scale(ka, p.err);
         sc[lane + 32] = good_scale(kb, p.err);
         sc[64 + lane] = ra;
         sc[64 + lane + 32] = rb;
-        sc[128 + lane] = fmaxf(log2f(ra), -64.f);
-        sc[128 + lane + 32] = fmaxf(log2f(rb), -64.f);
+        sc[128 + lane] = fmaxf(log2f(ra), -kMaxRatio);
+        sc[128 + lane + 32] = fmaxf(log2f(rb), -kMaxRatio);
         if (lane == 0) sc[192] = vref;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&B->sc_full[n & (kScaleBufs - 1)]));

@@ -69,6 +69,25 @@ def test_verify_any_scale_and_large_and_small_values():
     check_verify(case, 8, 2, *res)
 
 
+def test_verify_v_scales_that_grow_along_a_span():
+    """Runs of four tiles (a chunk) with V scales of 2^-119 before a tile of ordinary ones, several
+    chunks to a span; one page far above; scales above 2^48 are reported and taken as that."""
+    case = KV8Case(8, 128, [9000, 12000, 7000, 10000, 30000], 7, seed=23).cuda(32)
+    for r in range(case.nr):
+        pages = [int(x) for i, x in enumerate(case.pt[r]) if x >= 0 and i // 8 % 5 < 4]
+        case.v_scale[torch.tensor(pages, device="cuda")] = 2.0 ** -119
+    case.v_scale[int(case.pt[2, 120]), 1] = 2.0 ** 40
+    case.v_scale[int(case.pt[1, 3])] = 2.0 ** -100
+    res = run_verify(case, 32, 6, seed=11, scores=False)
+    assert s3r.s3r_get_error(case.ws) == 0
+    check_verify(case, 32, 6, *res)
+    case.v_scale[int(case.pt[1, 7]), 0] = 2.0 ** 60
+    res = run_verify(case, 32, 6, seed=11, scores=False)
+    assert s3r.s3r_get_error(case.ws) == 1 << 6
+    case.v_scale[int(case.pt[1, 7]), 0] = 2.0 ** 48
+    check_verify(case, 32, 6, *res)
+
+
 def test_verify_one_dominant_position_and_constant_values():
     """A key far above the rest (its weight 1, the others' 2^-18 each) and values of one sign, so
     that small weights' roundings would add up."""

@@ -79,7 +79,7 @@ def test_append_refusals():
         return s3r.lib.s3r_kv8_append(ctypes.byref(c or _cache()), ctypes.byref(b or _batch()), first, T, n_new, k, v, stride, ws, n, None)
 
     assert append(T=0) == OK and append(b=_batch(batch=0)) == OK
-    assert append(T=-1) == ARG and append(k=None) == ARG and append(v=0x24) == ARG
+    assert append(T=-1) == ARG and append(T=1 << 30) == ARG and append(k=None) == ARG and append(v=0x24) == ARG
     assert append(first=0x11) == ARG and append(n_new=0x12) == ARG
     assert append(stride=7 * 8 * 128 - 8) == ARG and append(stride=7 * 8 * 128 + 4) == ARG
     assert append(c=_cache(k_scale=None)) == ARG and append(ws=None) == WS and append(n=8) == WS
