@@ -178,7 +178,7 @@ def make_batch(seq_lens: torch.Tensor, page_table: torch.Tensor | None = None,
                      _ptr(seq_lens, torch.int32, "seq_lens").value,
                      pt.value if pt is not None else None, mp)
     desc._refs = (seq_lens, page_table, req_ids)
-    desc._device = seq_lens.device
+    desc._dev = seq_lens.get_device()
     return desc
 
 
@@ -294,42 +294,42 @@ def s3r_sparse_draft_attn(cache, batch, draft_step, q, k_new, v_new, sel_idx, se
         _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)), "s3r_sparse_draft_attn")
 
 # ------------------------------------------------------------- 8-bit cache, page tables ----
-def _arg(t, dtype, shape, what, device, allow_none=False):
-    """Address of a contiguous CUDA tensor of this dtype, shape and device. `dtype` may be a
-    tuple of accepted dtypes."""
+# (These checks run on every call, and a small call's time is the host's: identities before
+# comparisons, the device as an index, the shape last.)
+def _arg(t, dtype, shape, what, dev, allow_none=False):
+    """Address of a contiguous tensor of this dtype and shape (None: any) on CUDA device `dev`.
+    `dtype` may be a tuple of accepted dtypes."""
     if t is None:
         if allow_none:
             return None
         raise ValueError(f"{what} is required")
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what} must be a torch.Tensor")
-    if t.dtype != dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
+    if t.dtype is not dtype and not (type(dtype) is tuple and t.dtype in dtype):
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
-    if t.device != device:
-        raise ValueError(f"{what} must be on {device}, is on {t.device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{what} must be on cuda:{dev}, is on {t.device}")
     return t.data_ptr()
 
 
 def _call_device(*descs):
-    """The device of the descriptors' tensors, which must be the current one (the stream and the
-    launch are the current device's)."""
-    device = descs[0]._device
+    """The index of the device of the descriptors' tensors, which must be the current one (the
+    stream and the launch are the current device's)."""
+    dev = descs[0]._dev
     for d in descs[1:]:
-        if d._device != device:
+        if d._dev != dev:
             raise ValueError("cache and batch are on different devices")
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
-    return device
+    if dev != torch._C._cuda_getDevice():   # (torch.cuda.current_device without its set-up check)
+        raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    return dev
 
 
-def _ws_arg(ws, device):
-    if not isinstance(ws, torch.Tensor) or ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != device:
-        raise TypeError(f"ws must be a contiguous uint8 tensor on {device}")
-    return ws.data_ptr(), ws.numel()
+def _ws_arg(ws, dev):
+    return _arg(ws, torch.uint8, None, "ws", dev), ws.numel()
 
 
 def _batch_table(batch):
@@ -348,9 +348,9 @@ def _batch_table(batch):
     return batch._table
 
 
-def _stream_ptr(stream):
+def _stream_ptr(stream, dev):
     if stream is None:   # the handle alone: a Stream object takes a microsecond
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(dev)
     return stream.cuda_stream
 
 
@@ -364,12 +364,12 @@ def make_kv8_cache(k_pool: torch.Tensor, v_pool: torch.Tensor, k_scale: torch.Te
     if k_pool.device.type != "cuda":
         raise ValueError("k_pool must be a CUDA tensor")
     P, H, S, D = k_pool.shape
-    dev = k_pool.device
+    dev = k_pool.get_device()
     kp, vp = _arg(k_pool, f8, k_pool.shape, "k_pool", dev), _arg(v_pool, f8, k_pool.shape, "v_pool", dev)
     ks, vs = (_arg(t, torch.float32, (P, H), n, dev) for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")))
     desc = KV8CacheDesc(KVCacheDesc(num_q_heads, H, D, S, P, kp, vp), ks, vs)
     desc._refs = (k_pool, v_pool, k_scale, v_scale)
-    desc._device = dev
+    desc._dev = dev
     return desc
 
 
@@ -392,8 +392,8 @@ def s3r_kv8_append(cache, batch, k_new, v_new, ws, *, first=None, n_new=None, st
     T, inner = k_new.shape[1], (c.num_kv_heads * c.head_dim, c.head_dim, 1)
     stride = None
     for t, what in ((k_new, "k_new"), (v_new, "v_new")):
-        if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.device != dev:
-            raise TypeError(f"{what} must be a bf16 tensor on {dev}")
+        if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.get_device() != dev:
+            raise TypeError(f"{what} must be a bf16 tensor on cuda:{dev}")
         if t.shape != (nr, T, c.num_kv_heads, c.head_dim):
             raise ValueError(f"{what} must be [{nr}][{T}][{c.num_kv_heads}][{c.head_dim}], got {tuple(t.shape)}")
         if t.numel() and any(n > 1 and s != w for n, s, w in zip(t.shape[1:], t.stride()[1:], inner)):
@@ -407,7 +407,7 @@ def s3r_kv8_append(cache, batch, k_new, v_new, ws, *, first=None, n_new=None, st
     _check(_lib.s3r_kv8_append(
         ctypes.byref(cache), ctypes.byref(batch), _arg(first, i32, (nr,), "first", dev, True), T,
         _arg(n_new, i32, (nr,), "n_new", dev, True), k_new.data_ptr(), v_new.data_ptr(), stride, wp, wn,
-        _stream_ptr(stream)), "s3r_kv8_append")
+        _stream_ptr(stream, dev)), "s3r_kv8_append")
 
 
 def s3r_verify_attn_kv8(cache, batch, k, q, out, lse, score_logits, ws, stream=None):
@@ -424,7 +424,7 @@ def s3r_verify_attn_kv8(cache, batch, k, q, out, lse, score_logits, ws, stream=N
         ctypes.byref(cache), ctypes.byref(batch), k, _arg(q, bf, rows, "q", dev), _arg(out, bf, rows, "out", dev),
         _arg(lse, f32, rows[:3], "lse", dev),
         _arg(score_logits, f32, (nr, c.num_kv_heads, G * T, pt.shape[1] * PAGE_SIZE), "score_logits", dev, True),
-        wp, wn, _stream_ptr(stream)), "s3r_verify_attn_kv8")
+        wp, wn, _stream_ptr(stream, dev)), "s3r_verify_attn_kv8")
 
 
 def s3r_sparse_draft_attn_kv8(cache, batch, draft_step, q, sel_idx, sel_count, out, lse, ws, stream=None):
@@ -434,8 +434,8 @@ def s3r_sparse_draft_attn_kv8(cache, batch, draft_step, q, sel_idx, sel_count, o
     nr, _ = _batch_table(batch)
     c = cache.pools
     i32, rows = torch.int32, (nr, c.num_q_heads, c.head_dim)
-    if not isinstance(q, torch.Tensor) or q.dtype != torch.bfloat16 or q.device != dev:
-        raise TypeError(f"q must be a bf16 tensor on {dev}")
+    if not isinstance(q, torch.Tensor) or q.dtype is not torch.bfloat16 or q.get_device() != dev:
+        raise TypeError(f"q must be a bf16 tensor on cuda:{dev}")
     if q.shape != rows or any(n > 1 and s != w for n, s, w in zip(rows[1:], q.stride()[1:], (c.head_dim, 1))):
         raise ValueError(f"q must be {list(rows)} with contiguous rows, got {tuple(q.shape)}")
     if not isinstance(sel_idx, torch.Tensor) or sel_idx.dim() != 3:
@@ -447,7 +447,7 @@ def s3r_sparse_draft_attn_kv8(cache, batch, draft_step, q, sel_idx, sel_count, o
         _arg(sel_idx, i32, (nr, c.num_kv_heads, sel_idx.shape[2]), "sel_idx", dev), sel_idx.shape[2],
         _arg(sel_count, i32, (nr, c.num_kv_heads), "sel_count", dev),
         _arg(out, torch.bfloat16, rows, "out", dev), _arg(lse, torch.float32, rows[:2], "lse", dev, True),
-        wp, wn, _stream_ptr(stream)), "s3r_sparse_draft_attn_kv8")
+        wp, wn, _stream_ptr(stream, dev)), "s3r_sparse_draft_attn_kv8")
 
 
 def s3r_pages_workspace_size(num_requests: int) -> int:
@@ -464,7 +464,7 @@ def _pages_args(batch, held, free_pages, free_count, held_out, free_count_out):
     if not isinstance(free_pages, torch.Tensor) or free_pages.dim() != 1:
         raise ValueError("free_pages must be one-dimensional")
     return (dev, nr, pt.data_ptr(), _arg(held, i32, (nr,), "held", dev),
-            _arg(free_pages, i32, free_pages.shape, "free_pages", dev),
+            _arg(free_pages, i32, None, "free_pages", dev),
             _arg(free_count, i32, (1,), "free_count", dev), free_pages.shape[0],
             _arg(held_out, i32, (nr,), "held_out", dev), _arg(free_count_out, i32, (1,), "free_count_out", dev))
 
@@ -478,7 +478,7 @@ def s3r_alloc_pages(batch, T, held, free_pages, free_count, held_out, free_count
     _check(_lib.s3r_alloc_pages(
         ctypes.byref(batch), pt, T, _arg(n_new, torch.int32, (nr,), "n_new", dev, True), hp, fp, fc, cap, ho, fo,
         _arg(granted, torch.int32, (nr,), "granted", dev),
-        _arg(slot_map, torch.int64, (nr, T), "slot_map", dev, True), wp, wn, _stream_ptr(stream)), "s3r_alloc_pages")
+        _arg(slot_map, torch.int64, (nr, T), "slot_map", dev, True), wp, wn, _stream_ptr(stream, dev)), "s3r_alloc_pages")
 
 
 def s3r_release_pages(batch, held, free_pages, free_count, held_out, free_count_out, ws, *, keep_len=None,
@@ -488,7 +488,7 @@ def s3r_release_pages(batch, held, free_pages, free_count, held_out, free_count_
     wp, wn = _ws_arg(ws, dev)
     _check(_lib.s3r_release_pages(
         ctypes.byref(batch), pt, _arg(keep_len, torch.int32, (nr,), "keep_len", dev, True), hp, fp, fc, cap, ho, fo,
-        wp, wn, _stream_ptr(stream)), "s3r_release_pages")
+        wp, wn, _stream_ptr(stream, dev)), "s3r_release_pages")
 
 
 def _norms(t, what):
