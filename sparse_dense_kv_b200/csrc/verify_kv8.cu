@@ -41,7 +41,7 @@
 // spans per CTA down to single tiles, so that a few long requests use every SM.
 //   warp 0      claims spans, streams K tiles (2 KB per page, one TMA box of 16 KB when the 8 pages of
 //               a tile are consecutive), publishes each chunk's page scales, splits the next span's q
-//               rows into the K-major operand
+//               rows into the K-major operand (the first span's: warps 8-15)
 //   warp 1      streams V tiles, zeroing the rows behind the context's end (0 x NaN is NaN)
 //   warp 2      issues S^T tile (128 positions x 2 NP) = K . [qh, ql]^T, a ring of kNS tiles in
 //               tensor memory
@@ -50,8 +50,8 @@
 //   warps 8-15  second pass, two warpgroups of half the rows each (2 RP rows, the template parameter:
 //               no arithmetic on padding), one thread per position
 // Both passes in the same warps, one after the other, left QK idle during the second, PV during the
-// first, and every pipe waiting on one chain (331 us where this takes 303: 32 requests of 8K to
-// 24K tokens, 28 rows, no capture, one B200; 371 with capture; 4 rows 180, 96 % of the measured copy
+// first, and every pipe waiting on one chain (331 us where this takes 300: 32 requests of 8K to
+// 24K tokens, 28 rows, no capture, one B200; 360 with capture; 4 rows 181, 96 % of the measured copy
 // rate, where the softmax is short). What bounds 28 rows is the two
 // passes' instructions, each about 1500 cycles per tile where the copies take 1420, part of it
 // waiting for instructions to be fetched: the size of the code counts, hence the templates and the
@@ -70,7 +70,7 @@ using namespace tc;
 
 constexpr int kPos = 128;
 constexpr int kThreads = 512;
-constexpr int kPWarp0 = 8;                // second pass: 8 warps
+constexpr int kPWarp0 = 8, kPWarps = 8;   // second pass: 8 warps
 constexpr int kTileBytes = kPos * 128;    // 16 KB: 128 positions x 128 bytes (d = 64: half zero)
 constexpr int kRing = 16;
 constexpr int kScaleBufs = 8;             // chunks whose page scales are held
@@ -182,6 +182,7 @@ struct Bars {
   uint64_t qkd[kMaxSt], pvd[kMaxSt];
   uint64_t sempty[kMaxSt], pfull[kMaxSt];
   uint64_t q_full[2], q_empty[2];        // per span parity
+  uint64_t q0;                           // the first span's q rows
   uint64_t x_full[2], x_empty[2];        // per chunk parity: its logits are in tensor memory; have been read
   uint64_t sm_done[kScaleBufs];          // chunk's second pass is over
   uint64_t sc_full[kScaleBufs];          // chunk's page scales are in shared memory
@@ -352,6 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&B->sm_done[i]), 8);
     }
     mbar_init(smem_u32(&B->wg[2]), 4);
+    mbar_init(smem_u32(&B->q0), kPWarps);
     for (int i = 0; i < kRing; ++i) mbar_init(smem_u32(&B->item_bar[i]), 1);
     B->abort_flag = 0;
     fence_mbar_init();
@@ -361,6 +363,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(&B->tmem_base), 512);
     tmem_relinquish();
   }
+  for (int i = tid; i < 2 * C::kQBytes / 16; i += kThreads)   // operand rows that no q row fills stay zero
+    *reinterpret_cast<uint4*>(smem + C::kQOff + i * 16) = make_uint4(0, 0, 0, 0);
+  fence_proxy_async();
   __syncthreads();
   if (warp == 0) {
     const int per = (batch + 31) / 32;
@@ -411,6 +416,60 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   auto waitb = [&](uint64_t* bar, int phase) -> bool {
     return wait_warp(smem_u32(bar), (uint32_t)phase & 1u, abort_flag, p.err, p.wait_limit);
+  };
+
+  // q rows of span m -> operand buffer m & 1: a warp takes RI rows at a time, LR lanes to a row
+  // (8 elements each).
+  constexpr int LR = D / 8, RI = 32 / LR;
+  const int c8 = lane % LR;
+  auto load_q = [&](const Span& x, int j, int rows) -> uint4 {   // row j
+    if (j >= rows) return make_uint4(0, 0, 0, 0);
+    const int t = (x.g0 + j) / G, gq = x.g0 + j - t * G;
+    return *reinterpret_cast<const uint4*>(p.q + (((size_t)x.r * T + t) * p.Hq + x.kvh * G + gq) * D + c8 * 8);
+  };
+  auto split_row = [&](const uint4 raw, int j, int rows, int m) {
+    // largest |q| of the row by its bits (NaN above infinity above every finite value)
+    uint32_t a = __vmaxu2(__vmaxu2(raw.x & 0x7fff7fffu, raw.y & 0x7fff7fffu),
+                          __vmaxu2(raw.z & 0x7fff7fffu, raw.w & 0x7fff7fffu));
+    uint32_t amax = max(a & 0xffffu, a >> 16);
+#pragma unroll
+    for (int o = LR / 2; o; o >>= 1) amax = max(amax, __shfl_xor_sync(kFull, amax, o));
+    // the largest element's exponent goes to 2^7; a row of tiny values is not scaled past 2^120
+    const int e = max((int)(amax >> 7) - 127 - 7, -120);
+    const bool bad = amax >= 0x7f80u;   // NaN or infinity: the row's logits become NaN
+    const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    uint32_t hi[2], lo[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t hh = 0, ll = 0;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t v = w[2 * i + u];
+        const float f0 = __uint_as_float(v << 16) * inv, f1 = __uint_as_float(v & 0xffff0000u) * inv;
+        const uint32_t h2 = pack_e4m3(f0, f1);
+        const float2 hf = unpack_e4m3(h2);
+        const uint32_t l2 = pack_e4m3(f0 - hf.x, f1 - hf.y);
+        hh |= h2 << (16 * u);
+        ll |= l2 << (16 * u);
+      }
+      hi[i] = bad ? 0x7f7f7f7fu : hh;
+      lo[i] = bad ? 0x7f7f7f7fu : ll;
+    }
+    if (j < rows) {
+      const int w = j / NR, nh = w * NP + j - w * NR, nl = nh + NH;   // operand rows of the two parts
+      uint8_t* dst = smem + C::kQOff + (m & 1) * C::kQBytes + (c8 & 1) * 8;
+      *reinterpret_cast<uint2*>(dst + nh * 128 + (((c8 >> 1) ^ (nh & 7)) << 4)) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(dst + nl * 128 + (((c8 >> 1) ^ (nl & 7)) << 4)) = make_uint2(lo[0], lo[1]);
+      if (c8 == 0) {
+        rs[(m & 7) * NP + w * NH + j - w * NR] = __uint_as_float((uint32_t)(127 + e) << 23) * p.scale * kLog2e;
+        if (bad) set_error(p.err, S3R_ERR_NONFINITE);
+      }
+    }
+  };
+  auto zero_factors = [&](int rows, int m) {   // of the rows behind the last one
+#pragma unroll 1
+    for (int j = rows + lane; j < 2 * NR; j += 32) rs[(m & 7) * NP + j / NR * NH + j % NR] = 0.f;
   };
 
   if (warp <= 1) {
@@ -528,81 +587,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       return x.id >= 0;
     };
-    // q rows of span m -> buffer m & 1 (K producer), once the QK of span m - 2 has read it
-    constexpr int LR = D / 8;          // lanes per row (8 elements each)
-    constexpr int RI = 32 / LR;        // rows per pass
-    auto zero_q = [&]() {   // rows that no q row fills stay zero
-      for (int idx = lane; idx < 2 * C::kQBytes / 16; idx += 32)
-        *reinterpret_cast<uint4*>(smem + C::kQOff + idx * 16) = make_uint4(0, 0, 0, 0);
-    };
+    // q rows of span m (K producer, m > 0), once the QK of span m - 2 has read the buffer
     auto split_q = [&](const Span& x, int m) -> bool {
-      const int qb = m & 1;
-      if (m >= 2 && !waitb(&B->q_empty[qb], (m - 2) >> 1)) return false;
+      if (m >= 2 && !waitb(&B->q_empty[m & 1], (m - 2) >> 1)) return false;
       const int rows = min(p.Rg, R - x.g0);
       constexpr int kAhead = 8;   // loads in flight
-      uint4 rows_raw[kAhead];
+      uint4 raw[kAhead];
 #pragma unroll 1
       for (int jb = 0; jb < rows; jb += kAhead * RI) {
 #pragma unroll
+        for (int i = 0; i < kAhead; ++i) raw[i] = load_q(x, jb + i * RI + lane / LR, rows);
+#pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-          const int j = jb + i * RI + lane / LR, c8 = lane % LR;
-          rows_raw[i] = make_uint4(0, 0, 0, 0);
-          if (j < rows) {
-            const int t = (x.g0 + j) / G, gq = x.g0 + j - t * G;
-            rows_raw[i] = *reinterpret_cast<const uint4*>(p.q + (((size_t)x.r * T + t) * p.Hq + x.kvh * G + gq) * D + c8 * 8);
-          }
-        }
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int j0 = jb + i * RI;
-        if (j0 >= rows) break;
-        const int j = j0 + lane / LR, c8 = lane % LR;
-        const uint4 raw = rows_raw[i];
-        // largest |q| of the row by its bits (NaN above infinity above every finite value)
-        uint32_t a = __vmaxu2(__vmaxu2(raw.x & 0x7fff7fffu, raw.y & 0x7fff7fffu),
-                              __vmaxu2(raw.z & 0x7fff7fffu, raw.w & 0x7fff7fffu));
-        uint32_t amax = max(a & 0xffffu, a >> 16);
-#pragma unroll
-        for (int o = LR / 2; o; o >>= 1) amax = max(amax, __shfl_xor_sync(kFull, amax, o));
-        // the largest element's exponent goes to 2^7; a row of tiny values is not scaled past 2^120
-        const int e = max((int)(amax >> 7) - 127 - 7, -120);
-        const bool bad = amax >= 0x7f80u;   // NaN or infinity: the row's logits become NaN
-        const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-        uint32_t hi[2], lo[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t hh = 0, ll = 0;
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const uint32_t v = w[2 * i + u];
-            const float f0 = __uint_as_float(v << 16) * inv, f1 = __uint_as_float(v & 0xffff0000u) * inv;
-            const uint32_t h2 = pack_e4m3(f0, f1);
-            const float2 hf = unpack_e4m3(h2);
-            const uint32_t l2 = pack_e4m3(f0 - hf.x, f1 - hf.y);
-            hh |= h2 << (16 * u);
-            ll |= l2 << (16 * u);
-          }
-          hi[i] = bad ? 0x7f7f7f7fu : hh;
-          lo[i] = bad ? 0x7f7f7f7fu : ll;
-        }
-        if (j < rows) {
-          const int w = j / NR, nh = w * NP + j - w * NR, nl = nh + NH;   // operand rows of the two parts
-          uint8_t* dst = smem + C::kQOff + qb * C::kQBytes + (c8 & 1) * 8;
-          *reinterpret_cast<uint2*>(dst + nh * 128 + (((c8 >> 1) ^ (nh & 7)) << 4)) = make_uint2(hi[0], hi[1]);
-          *reinterpret_cast<uint2*>(dst + nl * 128 + (((c8 >> 1) ^ (nl & 7)) << 4)) = make_uint2(lo[0], lo[1]);
-          if (c8 == 0) {
-            rs[(m & 7) * NP + w * NH + j - w * NR] = __uint_as_float((uint32_t)(127 + e) << 23) * p.scale * kLog2e;
-            if (bad) set_error(p.err, S3R_ERR_NONFINITE);
-          }
+          if (jb + i * RI >= rows) break;
+          split_row(raw[i], jb + i * RI + lane / LR, rows, m);
         }
       }
-      }
-#pragma unroll 1
-      for (int j = rows + lane; j < 2 * NR; j += 32) rs[(m & 7) * NP + j / NR * NH + j % NR] = 0.f;
+      zero_factors(rows, m);
       fence_proxy_async();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&B->q_full[qb]));
+      if (lane == 0) mbar_arrive(smem_u32(&B->q_full[m & 1]));
       return true;
     };
     // The chunk after (x, t0): the next of the span, or the first of the next span.
@@ -614,11 +618,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       t0 = x.t0;
       t1 = min(t0 + C::kMT, x.t1);
       fetch_ids(x, t0, t1, ida, idb);
-      if (!is_v) {
-        zero_q();
-        __syncwarp();
-        if (!split_q(x, 0)) stop = true;
-      }
+      // the first span's q rows are the second pass's warps' (here: the barrier's phase)
+      if (!is_v && lane == 0) mbar_arrive(smem_u32(&B->q_full[0]));
     }
     // page scales of the next chunk (K producer), loaded while the current one streams
     float ka = 0.f, kb = 0.f, va = 0.f, vb = 0.f;
@@ -704,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int m = 0; ok; ++m) {
         Span x;
-        if (!ring_span(m, x) || !waitb(&B->q_full[m & 1], m >> 1)) break;
+        if (!ring_span(m, x) || !waitb(m == 0 ? &B->q0 : &B->q_full[m & 1], m >> 1)) break;
         const int tb = uni(x.t0), te = uni(x.t1);
         const uint64_t qm = qd + (m & 1) * (C::kQBytes >> 4);
 #pragma unroll 1
@@ -931,6 +932,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16);
     // 16-byte chunk XOR of this position's P^T row (32-, 64-byte swizzle)
     const int swz_row = NP == 16 ? ((lrow >> 2) & 1) : ((lrow >> 1) & 3);
+    // The first span's q rows, by all eight warps: the K producer, which splits the later spans' while
+    // their predecessors stream, is 4 us about 28 rows (4 requests of 40 tokens: 19.2 us by it, 14.8
+    // so, 15.7 by the first pass's four warps; 32 requests of 8K to 24K 371, 360 and 370).
+    {
+      Span x;
+      if (ring_span(0, x)) {
+        const int rows = min(p.Rg, R - x.g0), j = (warp - kPWarp0) * RI + lane / LR;
+        constexpr int kTimes = (2 * NR + kPWarps * RI - 1) / (kPWarps * RI);
+        uint4 raw[kTimes];
+#pragma unroll
+        for (int i = 0; i < kTimes; ++i) raw[i] = load_q(x, j + i * kPWarps * RI, rows);
+#pragma unroll
+        for (int i = 0; i < kTimes; ++i) split_row(raw[i], j + i * kPWarps * RI, rows, 0);
+        if (warp == kPWarp0) zero_factors(rows, 0);
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&B->q0));
+      }
+    }
     uint32_t wg_phase = 0;
     float orun[NR], lsum[NR];   // O of the span (this thread's d) and row sums, relative to the reference
     // Chunk n's O joins the span; with its last chunk the span's record (or, when the span is the
