@@ -90,6 +90,20 @@ def test_alloc_ragged_subset_in_place_and_again():
     assert s3r.s3r_get_error(p.ws) == 0
 
 
+@pytest.mark.parametrize("T", [511, 512, 513, 601, 4097, 8193])
+def test_alloc_long_slot_maps_of_odd_length(T):
+    """Slot rows that start at either half of 16 bytes, ragged, in segments of one to several CTAs; ids
+    out of order, and requests that the stack has no pages for."""
+    rng = np.random.default_rng(T)
+    lens, n = rng.integers(0, 40, size=9), rng.integers(0, T + 1, size=9)
+    n[2], n[5] = 0, T
+    p = Pool(lens, int(5 * T / 16), -(-(40 + T) // 16), seed=T)
+    ids = rng.permutation(9)[:7].tolist()
+    p.check_alloc(p.alloc(T, n, ids), T, n, ids)
+    p.check_alloc(p.alloc(T, n), T, n)
+    assert s3r.s3r_get_error(p.ws) == 0
+
+
 def test_alloc_reports_what_is_out_of_range():
     p = Pool([10, -3, 20, 30, 40], 10, 4, held=[1, 0, 2, 2, 9])
     n = np.array([5, 5, 61, 40, 3])     # 1: negative length; 2: more than T; 3: past four pages; 4: holds too many
