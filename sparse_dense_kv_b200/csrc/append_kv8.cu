@@ -63,7 +63,8 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_kv8_kernel(const App
   }
   const int start = L + f, end = start + n;
   const int pg = start / kPage + m;
-  if (pg * kPage >= end || h >= p.Hkv) return;
+  // (without rows the request's last page, which may be half full, receives none either)
+  if (n == 0 || pg * kPage >= end || h >= p.Hkv) return;
   const int page = p.page_table[(size_t)r * p.max_pages + pg];
   const int row0 = lane / LR, c8 = lane % LR;
   const bool any_old = pg * kPage < start;
