@@ -76,7 +76,10 @@ constexpr int kRing = 16;
 constexpr int kScaleBufs = 8;             // chunks whose page scales are held
 // V scales: vs / vref is at most 2^88, since vref >= 2^-40 and larger scales than 2^48 are refused,
 // and its logarithm counts as at least -88, so that the terms of a row sum lie between 2^-80 (a
-// logit at the reference's) and 2^96.
+// logit at the reference's) and 2^96. Between chunks and between spans the reference can rise by
+// 176 with the logits where they were. What such a step leaves of O is below 2^-38 of what joins it
+// (2^-126 times 2^88 of the spans' vref) and may go to zero; a row sum of 2^96 must come through
+// as 2^-80, so sums are scaled by 2^(step / 2) twice.
 constexpr float kMaxVScale = 0x1p48f, kMaxRatio = 88.f;
 constexpr int kScaleFloats = 196;         // ks, vs / vref, log2 of that (>= -kMaxRatio) [64] each; vref; pad
 constexpr int kMaxSt = 6;                 // ring stages
@@ -301,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
   float* redM = reinterpret_cast<float*>(smem + C::kRedOff);   // [2][4][NP] warp maxima (chunk parity)
   float* redL = redM + 2 * 4 * NP;                              // [2][8][NH] warp sums (span parity)
-  float* refs = redL + 2 * 8 * NH;                              // [4][3][NP] chunk & 3: -reference, O factor, reference
+  float* refs = redL + 2 * 8 * NH;                              // [4][3][NP] chunk & 3: -reference, root of the step, reference
   float* rs = refs + 4 * 3 * NP;                                // [8][NP] q row factor 2^e log2(e) / sqrt(d)
   float* scs = rs + 8 * NP;                                     // [8][196] page scales
   int* pref = reinterpret_cast<int*>(smem + C::kPrefOff);
@@ -916,7 +919,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (q4 == 0 && lane < 2 * NR) {
           float* rf = refs + (n & 3) * 3 * NP + jc;
           rf[0] = mn == -INFINITY ? 0.f : -mn;   // nothing seen yet: 2^-inf = 0
-          rf[NP] = first || mrun == -INFINITY ? 0.f : exp2f(mrun - mn);
+          rf[NP] = first || mrun == -INFINITY ? 0.f : exp2f(0.5f * (mrun - mn));
           rf[2 * NP] = mn;
         }
         mrun = mn;
@@ -974,7 +977,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int j = 0; j < NR; ++j) {
         const float v = fmaf(o[NH + j], 0.03125f, o[j]) * ov;
-        orun[j] = first ? v : fmaf(orun[j], rf[NP + j], v);
+        orun[j] = first ? v : fmaf(orun[j], rf[NP + j] * rf[NP + j], v);
       }
       if (!last) return true;
       Span x;
@@ -1037,8 +1040,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < RP; ++j) {
           nm[j] = *reinterpret_cast<const float2*>(rf + 2 * j);
           const float2 f = *reinterpret_cast<const float2*>(rf + NP + 2 * j);
-          lsum[2 * j] = first ? 0.f : lsum[2 * j] * f.x;
-          lsum[2 * j + 1] = first ? 0.f : lsum[2 * j + 1] * f.y;
+          const float2 ls = mul2(mul2(make_float2(lsum[2 * j], lsum[2 * j + 1]), f), f);
+          lsum[2 * j] = first ? 0.f : ls.x;
+          lsum[2 * j + 1] = first ? 0.f : ls.y;
         }
         // 2^(x - m), its sum in fp32, times vs / vref in two e4m3 parts to P^T. The next tile's logits
         // are on their way while this one is worked on, and a tile's P^T is handed over once the
@@ -1158,13 +1162,14 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kv8_kernel(const Verif
 #pragma unroll
   for (int i = 0; i < V; ++i) acc[i] = 0.f;
   for (int s0 = 0; s0 < nsp; s0 += 32) {
-    float w = 0.f, l = 0.f;
+    float h = 0.f, l = 0.f;   // root of the weight: see kMaxRatio
     if (s0 + lane < nsp) {
       const float ms = __ldcg(rec + (s0 + lane) * pitch + jr);
       l = __ldcg(rec + (s0 + lane) * pitch + p.Rp + jr);
-      w = ms == -INFINITY ? 0.f : exp2f(ms - M);
+      h = ms == -INFINITY ? 0.f : exp2f(0.5f * (ms - M));
     }
-    lsum = fmaf(w, l, lsum);
+    lsum = fmaf(h, h * l, lsum);
+    const float w = h * h;
     const int cnt = min(32, nsp - s0);
     const float* o = rec + s0 * pitch + 2 * p.Rp + (size_t)jr * D + lane * V;
     int u = 0;
