@@ -354,6 +354,17 @@ def _stream_ptr(stream, dev):
     return stream.cuda_stream
 
 
+def _request_stride(t, least, what):
+    """Elements between consecutive requests of t, whose per-request part has `least`. Requests that
+    share storage (t.expand) are refused: a stride of 0 means contiguous requests to the library."""
+    if t.shape[0] <= 1:
+        return least
+    stride = t.stride(0)
+    if stride < least:
+        raise ValueError(f"{what}: requests {stride} elements apart overlap (each has {least}); make it contiguous")
+    return stride
+
+
 def make_kv8_cache(k_pool: torch.Tensor, v_pool: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
                    num_q_heads: int) -> KV8CacheDesc:
     """Descriptor of an 8-bit cache: pools [num_pages][num_kv_heads][16][head_dim] of
@@ -398,7 +409,7 @@ def s3r_kv8_append(cache, batch, k_new, v_new, ws, *, first=None, n_new=None, st
             raise ValueError(f"{what} must be [{nr}][{T}][{c.num_kv_heads}][{c.head_dim}], got {tuple(t.shape)}")
         if t.numel() and any(n > 1 and s != w for n, s, w in zip(t.shape[1:], t.stride()[1:], inner)):
             raise ValueError(f"{what}: each request's rows must be contiguous")
-        own = t.stride(0) if nr > 1 else T * inner[0]
+        own = _request_stride(t, T * inner[0], what)
         if stride is not None and own != stride:
             raise ValueError("k_new and v_new must share a request stride")
         stride = own
@@ -443,7 +454,7 @@ def s3r_sparse_draft_attn_kv8(cache, batch, draft_step, q, sel_idx, sel_count, o
     wp, wn = _ws_arg(ws, dev)
     _check(_lib.s3r_sparse_draft_attn_kv8(
         ctypes.byref(cache), ctypes.byref(batch), _arg(draft_step, i32, (nr,), "draft_step", dev), q.data_ptr(),
-        q.stride(0) if nr > 1 else rows[1] * rows[2],
+        _request_stride(q, rows[1] * rows[2], "q"),
         _arg(sel_idx, i32, (nr, c.num_kv_heads, sel_idx.shape[2]), "sel_idx", dev), sel_idx.shape[2],
         _arg(sel_count, i32, (nr, c.num_kv_heads), "sel_count", dev),
         _arg(out, torch.bfloat16, rows, "out", dev), _arg(lse, torch.float32, rows[:2], "lse", dev, True),
