@@ -267,6 +267,17 @@ def s3r_select_pages_from_scores(cache, batch, scores, budget_bp, window, sel_id
                         window, sel_idx, sel_count, ws, stream)
 
 
+def _request_stride(t, least, what):
+    """Elements between consecutive requests of t, whose per-request part has `least`. Requests that
+    share storage (t.expand) are refused: a stride of 0 means contiguous requests to the library."""
+    if t.shape[0] <= 1:
+        return least
+    stride = t.stride(0)
+    if stride < least:
+        raise ValueError(f"{what}: requests {stride} elements apart overlap (each has {least}); make it contiguous")
+    return stride
+
+
 def _rows(t, inner, what):
     """Pointer and request stride (elements) of a [num_requests][...] view whose per-request
     part of `inner` elements is contiguous (e.g. block[:, i] of a [R][k+1][H][d] tensor)."""
@@ -274,7 +285,7 @@ def _rows(t, inner, what):
         raise TypeError(f"{what} must be a bf16 CUDA tensor")
     if t[0].numel() != inner or not t[0].is_contiguous():
         raise ValueError(f"{what}: each request's rows must be contiguous ({inner} elements)")
-    return ctypes.c_void_p(t.data_ptr()), int(t.stride(0)) if t.shape[0] > 1 else inner
+    return ctypes.c_void_p(t.data_ptr()), _request_stride(t, inner, what)
 
 
 def s3r_sparse_draft_attn(cache, batch, draft_step, q, k_new, v_new, sel_idx, sel_count, out,
@@ -352,17 +363,6 @@ def _stream_ptr(stream, dev):
     if stream is None:   # the handle alone: a Stream object takes a microsecond
         return torch._C._cuda_getCurrentRawStream(dev)
     return stream.cuda_stream
-
-
-def _request_stride(t, least, what):
-    """Elements between consecutive requests of t, whose per-request part has `least`. Requests that
-    share storage (t.expand) are refused: a stride of 0 means contiguous requests to the library."""
-    if t.shape[0] <= 1:
-        return least
-    stride = t.stride(0)
-    if stride < least:
-        raise ValueError(f"{what}: requests {stride} elements apart overlap (each has {least}); make it contiguous")
-    return stride
 
 
 def make_kv8_cache(k_pool: torch.Tensor, v_pool: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
