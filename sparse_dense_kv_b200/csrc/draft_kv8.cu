@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(128, kDraftKv8PerSm) draft_kv8_kernel(const Dr
     return;
   }
   const size_t rec_floats = (size_t)RW * (D + 2);
-  float* recs = p.part + ((size_t)bl * Hkv + kvh) * p.nchunk_max * rec_floats;
+  float* recs = p.part + ((size_t)(p.recs_by_id ? r : bl) * Hkv + kvh) * p.nchunk_max * rec_floats;
   slices_to_record<D, RW>(redO, fw, Mrow, Lrow, G, recs + c * rec_floats, tid, blockDim.x);
   if (!last_of(p.tickets + (size_t)r * Hkv + kvh, nch, &s_flag)) return;
   if (nch <= kDraftFastMerge) {
@@ -394,8 +394,10 @@ static int draft_kv8_chunks(int sel_stride, int chunk) {
   return (int)(((int64_t)sel_stride + S3R_MAX_K + chunk - 1) / chunk);
 }
 
-// Records of a launch over any `batch` <= num_requests requests: pairs * chunks, at most the
-// larger of what the longest chunk needs and two chunks more than a full grid per pair.
+// Records of a launch over any `batch` <= num_requests requests, which stand by their places in the
+// launch: pairs * chunks, at most the larger of what the longest chunk needs and two chunks more than
+// a full grid per pair. A longer list has ids out of range in it; its records stand by request
+// (recs_by_id), and its chunks are no shorter than those of num_requests requests.
 size_t draft_kv8_bytes(int num_requests, int Hkv, int sel_stride, int D, int num_sms) {
   const size_t pairs = (size_t)num_requests * Hkv;
   const size_t full = (size_t)kDraftKv8PerSm * num_sms + 2 * pairs;

@@ -164,7 +164,8 @@ struct DraftKv8Params {
   float scale;
   int* err;
   int* tickets;
-  float* part;             // chunk records [launch-local request][Hkv][nchunk_max]
+  float* part;             // chunk records [launch-local request, or request][Hkv][nchunk_max]
+  int recs_by_id;
   int chunk, nchunk_max;
   int num_requests;
 };

@@ -769,6 +769,7 @@ int s3r_sparse_draft_attn_kv8(const s3r_kv8_cache* cache, const s3r_batch* batch
   p.err = w.err;
   p.tickets = w.tickets;
   p.part = reinterpret_cast<float*>(w.part);
+  p.recs_by_id = batch->batch > batch->num_requests;
   p.chunk = draft_kv8_chunk(batch->batch * c->num_kv_heads, sel_stride, sms);
   p.num_requests = batch->num_requests;
   return finish(launch_draft_kv8(p, c->head_dim, batch->batch, (cudaStream_t)stream), 1);

@@ -5,6 +5,7 @@ import torch
 import sparse_dense_kv_b200 as s3r
 from tests.kv8_testlib import KV8Case
 from tests.test_gpu_kv8_append import assert_state, expect, rows, state
+from tests.test_gpu_kv8_attention import check_draft, draft_sets, run_draft
 
 pytestmark = pytest.mark.gpu
 
@@ -21,3 +22,23 @@ def test_append_of_no_rows_leaves_the_page_alone():
         s3r.s3r_kv8_append(case.cache, case.batch, kn, vn, case.ws, n_new=torch.tensor(n, dtype=torch.int32, device="cuda"))
         assert s3r.s3r_get_error(case.ws) == 0
         assert_state(case, expect(case, before, case.lens, n, kn, vn, range(4)))
+
+
+def test_draft_over_a_padded_list_of_requests():
+    """More ids than requests, those out of range reported and skipped: the real ones, at the list's
+    end and in sets of several chunks, use no more of the workspace than without the padding."""
+    case = KV8Case(2, 128, [900, 700, 1000, 30], 8, seed=14).cuda(8, sel_stride=1003)
+    idx, n = draft_sets(case, [900, 650, 1000, 30], seed=2)
+    assert idx.shape[2] == 1003
+    guard = torch.full((case.ws.numel() + (1 << 24),), 0x5A, dtype=torch.uint8, device="cuda")
+    need = s3r.s3r_kv8_workspace_size(case.cache, 4, case.max_pages, 0, 1, 1003)
+    ws, behind = guard[:need], guard[need:]
+    s3r.s3r_workspace_init(ws)
+    case.ws = ws
+    for pad in (0, 60, 1000):
+        ids = torch.tensor([-1, 4] * (pad // 2) + [2, 0, 3, 1], dtype=torch.int32, device="cuda")
+        batch = s3r.make_batch(case.seq_lens, case.page_table, req_ids=ids)
+        res = run_draft(case, 8, [2, 0, 1, 3], idx, n, seed=5, batch=batch)
+        assert s3r.s3r_get_error(ws) == (1 << 5 if pad else 0)
+        check_draft(case, 8, [2, 0, 1, 3], idx, n, *res)
+        assert (behind == 0x5A).all()
