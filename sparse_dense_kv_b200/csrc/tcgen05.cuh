@@ -92,14 +92,20 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float (&v)[N], bool
     run16(0);
   }
 }
+// N consecutive columns: 8, or a multiple of 16.
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[N]) {
+  static_assert(N == 8 || N % 16 == 0, "8 columns or whole groups of 16");
+  if constexpr (N == 8) {
+    tmem_ld8(taddr, v);
+  } else {
 #pragma unroll
-  for (int c = 0; c < N; c += 16) {
-    float w[16];
-    tmem_ld16(taddr + c, w);
+    for (int c = 0; c < N; c += 16) {
+      float w[16];
+      tmem_ld16(taddr + c, w);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[c + i] = w[i];
+      for (int i = 0; i < 16; ++i) v[c + i] = w[i];
+    }
   }
 }
 
