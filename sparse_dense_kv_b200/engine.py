@@ -192,7 +192,9 @@ class S3REngine:
 
     def prefill(self, q_x, k_x, v_x):
         """One-row dense pass of each request's pending token at position L (the last step of
-        a prefill): writes its K/V and the scores the first selection reads.
+        a prefill): writes its K/V and the scores the next selection reads. Between rounds too
+        (a slot went to a new request), for the whole batch again; rounds captured with
+        overlap_scores=False select from a verify's scores and are to be captured anew.
         q_x [NR][1][H_q][d], k_x / v_x [NR][1][H_kv][d]."""
         b = self.buf
         out = torch.empty_like(q_x)
@@ -202,6 +204,8 @@ class S3REngine:
         scores = b._scores[: NR * Hq * cap].view(NR, Hkv, Hq // Hkv, cap)   # one block row's layout
         self._verify_call(self.batch, 0, q_x, k_x, v_x, out, b.prefill_lse, scores)
         self.k_prev = 0
+        if self._scores_ready:   # the next round selects from position scores: these
+            L.s3r_position_scores(self.cache, self.batch, scores, b.prefill_lse, 0, self.pos_scores, self.ws)
         return out
 
     def select(self):
