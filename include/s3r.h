@@ -37,7 +37,9 @@
  *     0..batch-1, else req_ids[0..batch-1], which must be distinct and in [0, num_requests)
  *     (every kernel checks the range on the device: an id outside it sets
  *     S3R_ERR_DEVICE_BOUNDS and that request is skipped; s3r_commit, which has no error
- *     word, skips it). Every per-request array is indexed
+ *     word, skips it). An entry S3R_NO_REQUEST is empty: skipped and not reported, so that a
+ *     launch of a fixed number of entries (a captured one) covers a set of requests that the
+ *     device decides. Every per-request array is indexed
  *     by the request id (size num_requests), so a launch can cover a subset of a larger
  *     batch (mixed round phases).
  *     Attention and selection calls cover at most 65535 requests per launch.
@@ -79,6 +81,7 @@ typedef enum {
 #define S3R_MAX_K 8          /* draft length k <= 8 */
 #define S3R_MAX_GROUP 8      /* query heads per KV head */
 #define S3R_MAX_ROWS 64      /* G * (k + 1) rows of one KV head in a verify */
+#define S3R_NO_REQUEST (-0x40000000)   /* an empty entry of req_ids */
 
 typedef struct {
   int32_t num_q_heads;

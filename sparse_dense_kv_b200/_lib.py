@@ -24,6 +24,7 @@ STATUS_NAMES = {
 }
 PAGE_SIZE = 16
 MAX_K = 8
+NO_REQUEST = -(1 << 30)   # an empty entry of req_ids: skipped, not reported
 
 
 class S3RError(RuntimeError):

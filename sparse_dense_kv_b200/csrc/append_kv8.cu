@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_kv8_kernel(const App
   const int r = p.req_ids ? p.req_ids[bl] : bl;
   const bool teller = m == 0 && task == 0 && lane == 0;   // reports for the request
   if (r < 0 || r >= p.num_requests) {
-    if (teller) set_error(p.err, S3R_ERR_DEVICE_BOUNDS);
+    if (teller) no_request(r, p.err);
     return;
   }
   const int L = p.seq_lens[r];

@@ -37,6 +37,10 @@ __host__ __device__ inline size_t ws_tickets_bytes(int num_requests) {
 }
 
 __device__ __forceinline__ void set_error(int* err, int code) { atomicOr(err, 1 << code); }
+// An entry of req_ids outside the requests: reported unless it is an empty one.
+__device__ __forceinline__ void no_request(int r, int* err) {
+  if (r != S3R_NO_REQUEST) set_error(err, S3R_ERR_DEVICE_BOUNDS);
+}
 
 // ------------------------------------------------------------------------ PTX ----------
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {

@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(128) draft_kernel(const DraftParams p) {
   const int kvh = blockIdx.x, bl = blockIdx.y, c = blockIdx.z;
   const int r = p.req_ids ? p.req_ids[bl] : bl;
   if (r < 0 || r >= p.num_requests) {
-    if (c == 0 && kvh == 0 && tid == 0) set_error(p.err, S3R_ERR_DEVICE_BOUNDS);
+    if (c == 0 && kvh == 0 && tid == 0) no_request(r, p.err);
     return;
   }
   const int Hkv = p.Hkv, G = p.G;

@@ -26,8 +26,9 @@ constexpr int kPagesThreads = 256;
 constexpr int kAllocSeg = 4096;      // slots of a CTA's segment
 constexpr int kReleaseSeg = 1024;    // pages of a CTA's segment
 
+constexpr int kEmpty = -2;
 struct PageDemand {
-  int r;         // request, -1 if its id is out of range
+  int r;         // request; kEmpty, or -1 if its id is out of range
   int L, n;      // committed length, tokens (release: 0)
   int held, need, delta;   // pages held and wanted, demand
   bool bad;      // an input out of range: nothing changes hands
@@ -38,7 +39,7 @@ __device__ __forceinline__ PageDemand demand_of(const PagesParams& p, int b) {
   PageDemand d{};
   d.r = p.req_ids ? p.req_ids[b] : b;
   if (d.r < 0 || d.r >= p.num_requests) {
-    d.r = -1;
+    d.r = d.r == S3R_NO_REQUEST ? kEmpty : -1;
     d.bad = true;
     return d;
   }
@@ -109,7 +110,7 @@ __global__ void __launch_bounds__(kPagesThreads) pages_kernel(const PagesParams 
   if (tid < nb) {
     // not served: keeps what it has
     if (d.bad || (d.delta > 0 && before + d.delta > limit)) {
-      if (blockIdx.x == 0 && (d.bad || RELEASE)) set_error(p.err, S3R_ERR_DEVICE_BOUNDS);
+      if (blockIdx.x == 0 && d.r != kEmpty && (d.bad || RELEASE)) set_error(p.err, S3R_ERR_DEVICE_BOUNDS);
       d.bad = true;
       d.delta = 0;
     }

@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kSampThreads, kDsMinBlocks) draft_sample_kerne
   const int c = blockIdx.y, bl = blockIdx.x;
   const int r = p.req_ids ? p.req_ids[bl] : bl;
   if (r < 0 || r >= p.num_requests) {   // every CTA of the row returns: no ticket is touched
-    if (c == 0 && threadIdx.x == 0) set_error(p.err, S3R_ERR_DEVICE_BOUNDS);
+    if (c == 0 && threadIdx.x == 0) no_request(r, p.err);
     return;
   }
   const int i = p.draft_step[r];
@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(kSampThreads) spec_norm_kernel(const SamplePar
   const int bl = blockIdx.x, rw = blockIdx.y, c = blockIdx.z;
   const int r = p.req_ids ? p.req_ids[bl] : bl;
   if (r < 0 || r >= p.num_requests) {   // every CTA of the request returns
-    if (rw == 0 && c == 0 && threadIdx.x == 0) set_error(p.err, S3R_ERR_DEVICE_BOUNDS);
+    if (rw == 0 && c == 0 && threadIdx.x == 0) no_request(r, p.err);
     return;
   }
   const int k = p.k, V = p.vocab, nrows = 2 * k + 1;
@@ -659,7 +659,7 @@ __global__ void __launch_bounds__(kSampThreads) argmax_kernel(const SampleParams
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = p.req_ids ? p.req_ids[bl] : bl;
   if (r < 0 || r >= p.num_requests) {   // every CTA of the request returns
-    if (j == 0 && c == 0 && threadIdx.x == 0) set_error(p.err, S3R_ERR_DEVICE_BOUNDS);
+    if (j == 0 && c == 0 && threadIdx.x == 0) no_request(r, p.err);
     return;
   }
   const int k = p.k, V = p.vocab;

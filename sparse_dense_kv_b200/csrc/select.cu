@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectP
   }
   const int r = p.req_ids ? p.req_ids[bl] : bl;
   if (r < 0 || r >= p.num_requests) {
-    if (kvh == 0 && tid == 0) set_error(p.err, S3R_ERR_DEVICE_BOUNDS);
+    if (kvh == 0 && tid == 0) no_request(r, p.err);
     return;
   }
   const int L = p.seq_lens[r];
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kSigmaThreads) sigma_kernel(const SelectParams
   const int r = p.req_ids ? p.req_ids[bl] : bl;
   if (r < 0 || r >= p.num_requests) {
     // reported by the select kernel on its path; here for the scores-only call
-    if (p.window == 0 && blockIdx.x == 0 && kvh == 0 && threadIdx.x == 0) set_error(p.err, S3R_ERR_DEVICE_BOUNDS);
+    if (p.window == 0 && blockIdx.x == 0 && kvh == 0 && threadIdx.x == 0) no_request(r, p.err);
     return;
   }
   const int L = p.seq_lens[r];

@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(MAXT) verify_kernel(const __grid_constant__ CU
   const int bl = blockIdx.z, kvh = blockIdx.y, c = blockIdx.x;
   const int r = p.req_ids ? p.req_ids[bl] : bl;
   if (r < 0 || r >= p.num_requests) {
-    if (c == 0 && kvh == 0 && tid == 0) set_error(p.err, S3R_ERR_DEVICE_BOUNDS);
+    if (c == 0 && kvh == 0 && tid == 0) no_request(r, p.err);
     return;
   }
   const int L = p.seq_lens[r];

@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool known = r >= 0 && r < p.num_requests;
     const int L = known ? p.seq_lens[r] : -1;
     const bool fits = L >= 0 && L <= p.cap - T;
-    if (!fits && blockIdx.x == 0) set_error(p.err, S3R_ERR_DEVICE_BOUNDS);
+    if (!fits && blockIdx.x == 0) no_request(r, p.err);
     rid_s[b] = known ? r : 0;
     lens_s[b] = L;
     pref[b + 1] = fits ? (L + T + kPos - 1) / kPos : 0;   // tiles, turned into span counts below

@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     lens_s[b] = L;
     int items = 0;
     if (L >= 0 && Lc <= p.cap) items = Hkv * ((Lc + chunk - 1) / chunk);
-    else if (blockIdx.x == 0) set_error(p.err, S3R_ERR_DEVICE_BOUNDS);
+    else if (blockIdx.x == 0) no_request(r, p.err);
     pref[b + 1] = items;
   }
   __syncthreads();
