@@ -295,7 +295,9 @@ S3R_API size_t s3r_pages_workspace_size(int32_t num_requests);
  * new page of a request, after the `before` pages its predecessors in the batch asked for, is
  * free_pages[free_count - 1 - before - i], entered at page_table[r][held[r] + i]. A request
  * whose pages would go past the stack's last one gets none, nor do later ones that need any:
- * granted[r] = 0, no error (1 for every request that has its pages).
+ * granted[r] = 0, no error (1 for every request that has its pages). Leave such a request out of
+ * the calls that write rows (an S3R_NO_REQUEST entry, say): its table entries from held[r] on are
+ * old ones, of pages that other requests may hold by now.
  *   slot_map  int64 [num_requests][T] or NULL: page * 16 + slot of position L + t for
  *             t < n_new[r], -1 for the other t and for requests not served.
  * seq_lens, n_new or held out of range, or more pages than max_pages_per_req, leave the
@@ -310,7 +312,8 @@ S3R_API int s3r_alloc_pages(const s3r_batch* batch, int32_t* page_table, int32_t
 /* Pages back to the stack: request r keeps min(held[r], ceil(keep_len[r] / 16)) pages
  * (keep_len == NULL: none) and the others, in table order, go to free_pages[free_count +
  * before + i]. The table's entries stay as they are (those at held_out[r] and after mean
- * nothing). A request whose pages do not fit below free_capacity keeps them, as do later ones
+ * nothing). A page that several requests hold is pushed once for each that lets go of it, so all
+ * but the last one must keep it (keep_len). A request whose pages do not fit below free_capacity keeps them, as do later ones
  * that have any to give (S3R_ERR_DEVICE_BOUNDS); held or keep_len out of range likewise.
  * batch->seq_lens is not read. */
 S3R_API int s3r_release_pages(const s3r_batch* batch, const int32_t* page_table,

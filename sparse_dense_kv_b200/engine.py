@@ -73,7 +73,11 @@ class PagePool:
     """The pages of a pool that no request holds, as a stack on the GPU, and how many leading
     entries of its page-table row each request holds: `grow` and `release` are one launch each on
     the current stream and can be captured, so tables follow the lengths without the host.
-    Pages [0, num_pages) start free; the page table's entries are the pool's to write."""
+    Pages [0, num_pages) start free; the page table's entries are the pool's to write.
+
+    A request that `grow` does not serve (granted[r] = 0) has no pages for its next rows: the entries
+    of its row from held[r] on are old ones, of pages that others may hold by now. Calls that write
+    rows must leave it out; `served` gives the request list that does."""
 
     def __init__(self, num_pages, page_table):
         dev, nr = page_table.device, page_table.shape[0]
@@ -83,15 +87,32 @@ class PagePool:
         self.held = torch.zeros((nr,), dtype=torch.int32, device=dev)
         self.granted = torch.zeros((nr,), dtype=torch.int32, device=dev)
         self.ws = L.new_workspace(L.s3r_pages_workspace_size(nr), dev)
+        # entry r of a request list: none + granted[r] * to_id[r]
+        self._none = torch.full((nr,), L.NO_REQUEST, dtype=torch.int32, device=dev)
+        self._to_id = torch.arange(nr, dtype=torch.int32, device=dev) - L.NO_REQUEST
+
+    def _own(self, batch):
+        if batch.page_table != self.page_table.data_ptr():
+            raise ValueError("the batch's page table is not this pool's")
 
     def grow(self, batch, T, n_new=None, slot_map=None):
         """Room for T (or n_new[r] <= T) tokens behind each request's committed length; granted[r]
         says which requests have it (the stack may run out; see s3r_alloc_pages)."""
+        self._own(batch)
         L.s3r_alloc_pages(batch, T, self.held, self.free_pages, self.free_count, self.held, self.free_count,
                           self.granted, self.ws, n_new=n_new, slot_map=slot_map)
 
+    def served(self, out=None):
+        """int32 [NR] request list: entry r is r if granted[r], else NO_REQUEST (empty). A batch over
+        it covers the requests that have their pages; written on the GPU, so also in a captured
+        step."""
+        return torch.addcmul(self._none, self.granted, self._to_id, out=out)
+
     def release(self, batch, keep_len=None):
-        """Pages past ceil(keep_len[r] / 16) (None: all) of the batch's requests go back."""
+        """Pages past ceil(keep_len[r] / 16) (None: all) of the batch's requests go back. Pages that
+        requests share go back once for each that lets go of them: all but the last one must keep
+        them."""
+        self._own(batch)
         L.s3r_release_pages(batch, self.held, self.free_pages, self.free_count, self.held, self.free_count, self.ws,
                             keep_len=keep_len)
 
@@ -106,7 +127,12 @@ class S3REngine:
     With k_scale and v_scale (fp32 [num_pages][num_kv_heads]) the pools are an 8-bit cache
     (torch.float8_e4m3fn or uint8 codes): every row enters by s3r_kv8_append and the attention
     calls are the kv8 ones; selection, sampling and commit are the same. With pages (a PagePool
-    over page_table) every prefill and round first grows the page tables by the rows it writes."""
+    over page_table) every prefill and round first grows the page tables by the rows it writes.
+    A request that the pool refuses takes no part in that round: nothing of it is written, its
+    length stands and its n_out is 0 (pages.granted says which), and it goes on in the first round
+    for which there are pages. A slot without a request (or with a finished one) is taken out with
+    set_active: it would get pages like any other. A request refused at its prefill drafts its
+    first round from a set that no scores chose."""
 
     def __init__(self, k_pool, v_pool, page_table, seq_lens, num_q_heads, *, k, budget_bp,
                  window, vocab, seed, sel_stride=None, greedy=False, page_select=False, k_max=None,
@@ -127,6 +153,8 @@ class S3REngine:
             self.cache8 = L.make_kv8_cache(k_pool, v_pool, k_scale, v_scale, num_q_heads)
         if pages is not None and pages.page_table is not page_table:
             raise ValueError("pages must be the PagePool of this page table")
+        if pages is not None and pages.free_pages.numel() > k_pool.shape[0]:
+            raise ValueError("the PagePool has more pages than the cache")
         self.pages = pages
         # selection takes the pools' shape only: the same calls serve both caches
         self.cache = self.cache8.pools if self.cache8 is not None else L.make_cache(k_pool, v_pool, num_q_heads)
@@ -142,7 +170,16 @@ class S3REngine:
         size, cache = (L.s3r_workspace_size, self.cache) if self.cache8 is None else (L.s3r_kv8_workspace_size, self.cache8)
         nbytes = size(cache, self.num_requests, self.max_pages, k_max, vocab, self.sel_stride)
         self.ws = L.new_workspace(nbytes, k_pool.device)
-        self.batch = L.make_batch(seq_lens, page_table)
+        # with a page pool: the slots in use, and those of them that have their pages in this round
+        self._slots = self._live = None
+        if pages is not None:
+            self._slots = torch.arange(self.num_requests, dtype=torch.int32, device=k_pool.device)
+            self._live = self._slots.clone()
+            self._slot_batch = L.make_batch(seq_lens, page_table, req_ids=self._slots)
+            # what a request selects from whose verify has not written scores yet: all equal
+            self.buf._scores.zero_()
+            self.buf._lse.fill_(float("inf"))
+        self.batch = L.make_batch(seq_lens, page_table, req_ids=self._live)
         # The next selection's position scores (s3r_position_scores) are computed on a second
         # stream while speculative sampling and the commit run on this one; they read the
         # lengths from a snapshot taken before the fork, so the commit never races them.
@@ -152,7 +189,9 @@ class S3REngine:
             self.pos_scores = torch.empty((self.num_requests, self.cache.num_kv_heads, self.cap),
                                           dtype=torch.float32, device=k_pool.device)
             self._len_snap = torch.empty_like(seq_lens)
-            self._snap_batch = L.make_batch(self._len_snap, page_table)
+            if pages is not None:
+                self.pos_scores.zero_()
+            self._snap_batch = L.make_batch(self._len_snap, page_table, req_ids=self._live)
             self._score_stream = torch.cuda.Stream(k_pool.device)
         self.k_prev = None
         self._verify_launches = 2
@@ -164,6 +203,23 @@ class S3REngine:
             raise ValueError("k outside 1..k_max")
         self.k = k
         self.buf.set_k(k)
+
+    def set_active(self, active):
+        """Which slots take part in the next prefills and rounds (a bool or 0 / 1 per slot, a list or a
+        tensor; all of them at first). On the current stream, and in force for rounds captured before."""
+        if self.pages is None:
+            raise ValueError("slots are taken out of an engine with a PagePool only")
+        on = torch.as_tensor(active, device=self._slots.device) != 0
+        if on.shape != self._slots.shape:
+            raise ValueError(f"active must have shape ({self.num_requests},), got {tuple(on.shape)}")
+        ids = torch.arange(self.num_requests, dtype=torch.int32, device=self._slots.device)
+        self._slots.copy_(ids.masked_fill_(~on, L.NO_REQUEST))
+
+    def _grow(self, T):
+        """Pages for T rows of the active slots; the batch of the calls that follow are those served."""
+        self.pages.granted.zero_()
+        self.pages.grow(self._slot_batch, T)
+        self.pages.served(out=self._live)
 
     @property
     def launches_per_round(self) -> int:
@@ -199,7 +255,9 @@ class S3REngine:
         b = self.buf
         out = torch.empty_like(q_x)
         if self.pages is not None:
-            self.pages.grow(self.batch, 1)
+            self._grow(1)
+            out.zero_()   # the rows of requests that take no part
+            b.prefill_lse.fill_(float("inf"))
         NR, Hq, Hkv, _, cap = b.dims
         scores = b._scores[: NR * Hq * cap].view(NR, Hkv, Hq // Hkv, cap)   # one block row's layout
         self._verify_call(self.batch, 0, q_x, k_x, v_x, out, b.prefill_lse, scores)
@@ -285,7 +343,8 @@ class S3REngine:
         if self.k_prev is None:
             raise RuntimeError("call prefill() before the first round")
         if self.pages is not None:
-            self.pages.grow(self.batch, self.k + 1)
+            self._grow(self.k + 1)
+            self.buf.n_out.zero_()
         self.select()
         for i in range(self.k):
             self.draft_step(i, q_block, k_block, v_block, q_logits, draft_logits_fn)
