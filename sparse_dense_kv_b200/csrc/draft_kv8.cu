@@ -308,15 +308,16 @@ __global__ void __launch_bounds__(128, kDraftKv8PerSm) draft_kv8_kernel(const Dr
     l0 += __shfl_xor_sync(kFull, l0, x);
     l1 += __shfl_xor_sync(kFull, l1, x);
   }
-  // O relative to the row maximum: 2^(mz - m - 10) (0 in a warp without positions)
-  const float v0 = m0 == -INFINITY && l0 == 0.f ? 0.f : ex2(z0 - m0 - 10.f);
-  const float v1 = m1 == -INFINITY && l1 == 0.f ? 0.f : ex2(z1 - m1 - 10.f);
+  // O relative to the row maximum: 2^(mz - m - 10) (0 in a warp without positions), by its root twice:
+  // the factor itself is no normal number where all V scales are below 2^-116
+  const float v0 = m0 == -INFINITY && l0 == 0.f ? 0.f : ex2(0.5f * (z0 - m0 - 10.f));
+  const float v1 = m1 == -INFINITY && l1 == 0.f ? 0.f : ex2(0.5f * (z1 - m1 - 10.f));
   float* ro = redO + (size_t)warp * RW * (D + 4);
 #pragma unroll
   for (int j = 0; j < MT; ++j) {
     const int d0 = g * (D / 8) + 2 * j;
-    *reinterpret_cast<float2*>(ro + (2 * t) * (D + 4) + d0) = make_float2(o[j][0] * v0, o[j][2] * v0);
-    *reinterpret_cast<float2*>(ro + (2 * t + 1) * (D + 4) + d0) = make_float2(o[j][1] * v1, o[j][3] * v1);
+    *reinterpret_cast<float2*>(ro + (2 * t) * (D + 4) + d0) = make_float2(o[j][0] * v0 * v0, o[j][2] * v0 * v0);
+    *reinterpret_cast<float2*>(ro + (2 * t + 1) * (D + 4) + d0) = make_float2(o[j][1] * v1 * v1, o[j][3] * v1 * v1);
   }
   if (g == 0) {
     redM[warp * RW + 2 * t] = m0;
