@@ -231,8 +231,15 @@ S3R_API int s3r_sparse_draft_attn(const s3r_kv_cache* cache, const s3r_batch* ba
  * L..L+k, which replaces the drafts' rows). Two requests that share a page may both read it;
  * a page that receives rows belongs to one request.
  *
+ * A page's rows share a scale, so a drafted row that raises it re-rounds the committed rows of its
+ * page: a code that leaves e4m3's normal range loses bits, at most 2^-10 of the new scale (2^-17 of
+ * the page's largest element), and does not get them back when the draft is rejected and its row
+ * overwritten. For the same reason row t of a verify reads committed rows as the block's later rows
+ * left them. Speculative sampling over this cache is exact up to that rounding.
+ *
  * Scales are >= 0 and finite; any other scale read is taken as 0 and sets S3R_ERR_NONFINITE.
- * s3r_kv8_append writes powers of two, the attention calls take any. */
+ * s3r_kv8_append writes powers of two (2^-126 to 2^120), the attention calls take any, but for one
+ * limit of the verify: see there. */
 typedef struct {
   s3r_kv_cache pools;        /* k_pool, v_pool: e4m3 [num_pages][num_kv_heads][16][head_dim], 16-byte aligned */
   float* k_scale;            /* [num_pages][num_kv_heads] */
@@ -265,8 +272,9 @@ S3R_API int s3r_kv8_append(const s3r_kv8_cache* cache, const s3r_batch* batch, c
 /* Dense verify attention over an 8-bit cache: rows t = 0..k of request r at positions L+t,
  * row t of each query head attending positions 0..L+t of the cache (k = 0: one decode row).
  * q, out, lse, score_logits as for s3r_verify_attn; sums, maxima and logits in fp32. V scales
- * above 2^48 (values of 10^17) are taken as 2^48 and set S3R_ERR_NONFINITE; a page whose V scale
- * is below 2^-88 of another's of its request and KV head may count as zeros. */
+ * above 2^48 (values of 10^17) are taken as 2^48 and set S3R_ERR_NONFINITE (the draft takes them as
+ * they are); the values of a page whose V scale is below 2^-88 of another's of its request and KV
+ * head may count as zeros (its weights count in the sums). */
 S3R_API int s3r_verify_attn_kv8(const s3r_kv8_cache* cache, const s3r_batch* batch, int32_t k,
                         const void* q, void* out, float* lse, float* score_logits, void* ws,
                         size_t ws_bytes, s3r_stream_t stream);

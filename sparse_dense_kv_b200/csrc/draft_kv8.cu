@@ -31,7 +31,10 @@
 // Measured: 32 requests of 8k to 24k, 8 KV heads, d = 128: 22 us at 5% of the cache (2.5 TB/s; the
 // bf16 draft takes 31), 77 us at 20% of 24k each (4.2 TB/s, 65% of the copy rate); 26 and 95 us
 // before the registers were refilled early. Chunks of up to 512 or 2048, twice the CTAs and loads
-// past L1 are not faster.
+// past L1 are not faster. What bounds the 5%: each warp's chain index -> page -> row and scale ->
+// product, once per 32 positions with one batch of rows in registers, and the split: the chunk follows
+// from the longest set (sel_stride), not the sets' sum, so the longest of the 400 CTAs has 768
+// positions where an even share of the 444 resident ones is 467.
 #include "attention.cuh"
 #include "draft_merge.cuh"
 #include "kernels.h"

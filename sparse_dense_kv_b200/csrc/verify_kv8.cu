@@ -1,6 +1,6 @@
 // Dense verify attention over the 8-bit cache (e4m3 codes, one scale per (page, KV head) for
 // K and for V) on the 5th-generation tensor cores, head_dim 64 and 128, up to 64 rows per KV
-// head (padded to NP = 16, 32, 48 or 64).
+// head (padded to NP = 16 or 32; more than 32 as two groups of half the rows).
 //
 // What it computes: row (t, g) of a request at committed length L attends positions 0..L+t of
 //   k_j = K[j] ks[page(j)],  v_j = V[j] vs[page(j)]
@@ -21,9 +21,9 @@
 //     whatever the page scales are (down to 2^-88 of vref). ph = e4m3(p),
 //     pl = e4m3(32 (p - ph)): within 2^-9 of p (bf16's half step is 2^-9 of the next power of
 //     two), and within 2^-23 of the largest p below the normal range.
-// The two parts stand side by side along N in both products (2 NP columns): an MMA of M = 128,
-// K = 32 takes 70 to 100 cycles at N = 32 and at N = 64 alike (measured), and the tensor pipe is
-// what a tile's 12 MMAs (both parts into one S) were waiting for; with 8 the softmax is.
+// The two parts stand side by side along N in both products (2 NP columns), so that a tile takes 8
+// MMAs of M = 128, K = 32, not 12 (both parts into one S): 49 cycles each at N = 64 (measured), some
+// 390 of the 2500 that a tile of 28 rows takes.
 // The scales enter in fp32: ks times the logit of its position (one tensor-memory lane = one
 // position = one page), vs / vref into p, vref into O. The row sums are those of 2^(x - m) in fp32;
 // m need not be the row's maximum (it is within 96 of it).
@@ -51,12 +51,15 @@
 //               no arithmetic on padding), one thread per position
 // Both passes in the same warps, one after the other, left QK idle during the second, PV during the
 // first, and every pipe waiting on one chain (331 us where this takes 300: 32 requests of 8K to
-// 24K tokens, 28 rows, no capture, one B200; 360 with capture; 4 rows 181, 96 % of the measured copy
-// rate, where the softmax is short). What bounds 28 rows is the two
-// passes' instructions, each about 1500 cycles per tile where the copies take 1420, part of it
-// waiting for instructions to be fetched: the size of the code counts, hence the templates and the
-// cold parts out of line. All rings hand over tile by tile. Every wait is bounded
-// (S3R_ERR_TIMEOUT, as in verify_tc.cu).
+// 24K tokens, 28 rows, no capture, one B200; 362 with capture; 4 rows 181, 96 % of the measured copy
+// rate, where the softmax is short).
+// What bounds 28 rows: the copies take 1420 cycles of a tile's 2500. Each pass takes about 1500 beside
+// them, part of it waiting for instructions to be fetched (the size of the code counts, hence the
+// templates and the cold parts out of line); the rest is the chunk's boundary, where the second pass
+// waits for the chunk's maxima and the first for the logits' buffer. 16 rows show it: 191 us in chunks
+// of 8 tiles with four S slots, 238 in the instance of 20 rows (4 tiles, two slots). From there the
+// rows' arithmetic adds: 255 us at 20 rows, 290 at 24, 298 at 28. All rings hand over tile by tile.
+// Every wait is bounded (S3R_ERR_TIMEOUT, as in verify_tc.cu).
 #include <type_traits>
 
 #include "kernels.h"
@@ -1229,7 +1232,14 @@ static int launch_kv8_d(const CUtensorMap& k1, const CUtensorMap& v1, const CUte
                         const CUtensorMap& v8, const VerifyKv8Params& p, int batch, int num_sms,
                         cudaStream_t stream) {
   int st;
-  const int rp = (p.Rg + 3) / 4;   // pairs of rows per warpgroup, up to the next instance
+  // Pairs of rows per warpgroup, up to the next instance. Up to 4 pairs (16 rows) an instance is worth
+  // little without capture and up to 3 % with it: 4 rows take 181 us (196 with capture) in instance 1 and
+  // 183 (200) in 4, 8 rows 183 (206) in 2 and 186 (212) in 4, 12 rows 189 (222) in 4 and 187 (220) in one of
+  // their own, which is not built. Above, each is: 16 rows 191 (234) in 4 and 239 (278) in 5, 20 rows
+  // 254 (296) in 5 and 280 (333) in 7, 28 rows 298 (362) in 7 and 302 (460) in 8. An instance for 24 rows
+  // would take 280 (318) where 7 takes 290 (348); it is not built either.
+  // (32 requests of 8K to 24K tokens, 8 heads of 128, one B200.)
+  const int rp = (p.Rg + 3) / 4;
   if (rp <= 1) st = launch_kv8_t<1, D>(k1, v1, k8, v8, p, batch, num_sms, stream);
   else if (rp <= 2) st = launch_kv8_t<2, D>(k1, v1, k8, v8, p, batch, num_sms, stream);
   else if (rp <= 4) st = launch_kv8_t<4, D>(k1, v1, k8, v8, p, batch, num_sms, stream);

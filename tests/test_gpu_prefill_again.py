@@ -9,13 +9,12 @@ from tests.test_gpu_kv8_round import engine, tensors
 pytestmark = pytest.mark.gpu
 
 
-@pytest.mark.parametrize("kw", [dict(), dict(page_select=True), dict(overlap_scores=False)])
-@pytest.mark.parametrize("captured", [False, True])
-def test_the_round_after_another_prefill_selects_from_its_scores(kw, captured):
+# (a round captured without overlapped scores selects from a verify's: captured again after a prefill)
+@pytest.mark.parametrize("captured,kw", [(False, {}), (False, dict(page_select=True)), (False, dict(overlap_scores=False)),
+                                         (True, {}), (True, dict(page_select=True))])
+def test_the_round_after_another_prefill_selects_from_its_scores(captured, kw):
     """Two engines over equal caches do rounds, and then one of them is given another query for a
     prefill: the next round's sets are those of an engine whose first prefill it is."""
-    if captured and kw.get("overlap_scores") is False:
-        pytest.skip("a captured round without overlapped scores selects from a verify's: captured again after a prefill")
     k, dims = 3, (8, 2, 128)
     data = [tensors(3, k, *dims, 512, seed=40 + i) for i in range(3)]
 
