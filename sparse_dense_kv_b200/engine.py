@@ -319,6 +319,8 @@ class S3REngine:
 
     def sample_and_commit(self, p_logits, q_logits):
         b = self.buf
+        if self.pages is not None:
+            b.n_out.zero_()   # of the requests that took no part
         if self.overlap_scores:
             self.fork_scores(self.batch, self._snap_batch, self.k)
         if self.greedy:
@@ -344,7 +346,6 @@ class S3REngine:
             raise RuntimeError("call prefill() before the first round")
         if self.pages is not None:
             self._grow(self.k + 1)
-            self.buf.n_out.zero_()
         self.select()
         for i in range(self.k):
             self.draft_step(i, q_block, k_block, v_block, q_logits, draft_logits_fn)

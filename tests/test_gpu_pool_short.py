@@ -208,3 +208,48 @@ def test_pool_and_engine_refusals():
         s3r.S3REngine(*args, pages=big, **kw)
     with pytest.raises(ValueError):
         s3r.S3REngine(*args, **kw).set_active([1, 1, 1])              # no pool
+
+
+def test_prompts_of_a_whole_batch_are_admitted_as_far_as_the_pool_goes():
+    """One allocation and one append for all prompts over the served list, then rounds recorded by
+    S3REngine.capture; the prompt that found no pages is admitted when another one has ended."""
+    nr, total = 3, 6
+    pools = [torch.full((total, HKV, 16, D), 0x7F, dtype=torch.uint8, device="cuda") for _ in range(2)]     # NaN codes: nothing was written
+    scales = [torch.ones((total, HKV), device="cuda") for _ in range(2)]
+    table, lens = torch.full((nr, COLS), -1, dtype=torch.int32, device="cuda"), torch.zeros(nr, dtype=torch.int32, device="cuda")
+    pool, batch = s3r.PagePool(total, table), s3r.make_batch(lens, table)
+    n = torch.tensor([20, 70, 17], dtype=torch.int32, device="cuda")        # 2, 5 and 2 pages
+    pool.grow(batch, 70, n_new=n)
+    assert pool.granted.tolist() == [1, 0, 0] and pool.served().tolist() == [0, s3r.NO_REQUEST, s3r.NO_REQUEST]
+    pool.grow(s3r.make_batch(lens, table, req_ids=torch.tensor([2], dtype=torch.int32, device="cuda")), 70, n_new=n)
+    e = s3r.S3REngine(*pools, table, lens, HQ, k=K, budget_bp=5000, window=8, vocab=VOCAB, seed=5, k_scale=scales[0], v_scale=scales[1], pages=pool)
+    g = torch.Generator(device="cuda").manual_seed(7)
+    kp, vp = (torch.randn((nr, 70, HKV, D), generator=g, device="cuda").bfloat16() for _ in range(2))
+    assert pool.served().tolist() == [0, s3r.NO_REQUEST, 2]
+    s3r.s3r_kv8_append(e.cache8, s3r.make_batch(lens, table, req_ids=pool.served()), kp, vp, pool.ws, n_new=n)
+    lens.copy_(n * pool.granted)
+    e.set_active(pool.granted)
+    data = [tensors(nr, K, HQ, HKV, D, VOCAB, seed=110 + i) for i in range(2)]
+    e.prefill(*first(data[0]))
+    e.round(*data[1])
+    graph, launches = e.capture(lambda: e.round(*data[1]))                  # (runs the round once more)
+    assert launches == e.launches_per_round
+    graph.replay()
+    assert e.check_errors() == 0 and pool.check_errors() == 0
+    assert lens.tolist()[1] == 0 and e.buf.n_out[1] == 0 and min(lens.tolist()[::2]) >= 20
+    # the first ends
+    e.set_active([0, 0, 1])
+    pool.release(s3r.make_batch(lens, table, req_ids=torch.tensor([0], dtype=torch.int32, device="cuda")))
+    lens[0], n[1] = 0, 30
+    one = s3r.make_batch(lens, table, req_ids=torch.tensor([1], dtype=torch.int32, device="cuda"))
+    pool.grow(one, 70, n_new=n)
+    assert int(pool.granted[1]) == 1
+    s3r.s3r_kv8_append(e.cache8, one, kp, vp, e.ws, n_new=n)
+    lens[1] = 30
+    e.set_active([0, 1, 1])
+    e.prefill(*first(data[0]))
+    before = lens.tolist()
+    graph.replay()
+    assert e.check_errors() == 0 and pool.check_errors() == 0 and pool.granted.tolist() == [0, 1, 1]
+    assert lens.tolist()[0] == 0 and lens.tolist()[1] > 30 and lens.tolist()[2] > before[2] and int(pool.held[0]) == 0
+    assert not e.buf.verify_out[1:].isnan().any()
